@@ -91,8 +91,13 @@ enum {
     FS_VARIANT_GROUPED = 1,
     FS_VARIANT_TOPK = 2,
     FS_VARIANT_MULTINOMIAL = 3,
-    FS_VARIANT_LOGITS = 4
+    FS_VARIANT_LOGITS = 4,
+    FS_VARIANT_LOGPROBS = 5,  /* k: n_top                                       */
+    FS_VARIANT_EMBED_GRAD = 6
 };
+
+/* element types of the operators that take more than bfloat16 */
+enum { FS_F32 = 0, FS_BF16 = 1, FS_F16 = 2 };
 
 typedef struct {
     int32_t B;        /* rows of H (decode batch); 0 is a no-op                 */
@@ -256,6 +261,108 @@ fs_status fs_logits(const fs_params* p, const void* H, const void* W, float* log
 fs_status fs_multinomial(const fs_params* p, const float* logits, const float* temp,
                          const uint32_t* allow, int32_t* out_idx, void* ws, size_t ws_bytes,
                          void* stream);
+
+/* A W [V, d] held in 4 bits: weight (j, k) = scale[j, k / group] *
+ * (q[j, k] - zero[j, k / group]). */
+typedef struct {
+    const void* q;        /* device [V, d / 2] bytes, 16-byte aligned: byte i of a row
+                             holds q[j, 2i] in its low and q[j, 2i + 1] in its high
+                             four bits, each 0..15                               */
+    const void* scale;    /* device [V, d / group] of scale_dtype                */
+    const uint8_t* zero;  /* device [V, d / group], or NULL: 8 everywhere        */
+    int32_t group;        /* consecutive k that share a scale: 32, 64, or a
+                             multiple of 128; divides d                          */
+    int32_t scale_dtype;  /* FS_F32, FS_BF16 or FS_F16                           */
+} fs_quant;
+
+/* fs_logits_quant -- fs_logits from a 4-bit W: writes l[b, j] = sum_k H[b, k]
+ * w[j, k] (FP32 sums, no temperature, no mask) to device logits [B, V]
+ * row-major, ready for fs_multinomial and fs_logprobs.  Each group's sum of
+ * H q is formed first, in FP32, and scaled once, so the weights are never
+ * rounded to bfloat16.  H as defined above (finite values: an infinite or NaN
+ * H[b, k] makes row b NaN).  B, d, V of p are read; d must be a multiple of
+ * the group.  No workspace. */
+fs_status fs_logits_quant(const fs_params* p, const void* H, const fs_quant* W, float* logits,
+                          void* stream);
+
+/* fs_logprobs -- log probabilities of the tempered, masked softmax of given
+ * logits: p_i = exp(x_i) / sum exp(x), x = l / temp as in the shared
+ * definitions (greedy rows: x = l).  Reads every logit once.
+ *   logits       device, B rows of V elements of type `dtype` (FS_F32, FS_BF16,
+ *                FS_F16), row b at element b * ld; ld >= V.  +inf counts as the
+ *                largest finite FP32 value, NaN as masked.
+ *   token        device int32 [B], global ids, or NULL (then out_logprob and
+ *                out_rank must be NULL)
+ *   out_logprob  device float [B] or NULL: ln p of token[b]; -inf for a token
+ *                that is masked, negative or outside this call's V rows
+ *   out_rank     device int32 [B] or NULL: 1 + the number of unmasked ids that
+ *                come before the token by (larger logit, then lower id); 0
+ *                where out_logprob has no token to look at
+ *   out_lse      device float [B] or NULL: ln sum exp(x)
+ *   out_entropy  device float [B] or NULL: -sum p ln p
+ *   top_idx, top_logprob  device int32 / float [B, n_top]: the n_top ids that
+ *                come first in that order and their ln p; -1 and -inf past the
+ *                last unmasked id.  0 <= n_top <= 64 (FS_ERR_INVALID_ARG below,
+ *                FS_ERR_UNSUPPORTED above); both may be NULL if n_top is 0.
+ * A row with nothing unmasked has lse -inf, entropy 0 and no token or
+ * alternative.  Shards of one vocabulary (v_offset): with L = logaddexp of the
+ * shards' lse, a global ln p is the shard's ln p + lse - L, the global entropy
+ * the sum over shards of w (entropy + L - lse), w = exp(lse - L).
+ * ws: fs_workspace_bytes(p, FS_VARIANT_LOGPROBS, n_top) bytes; it needs no
+ * initialisation and keeps nothing between calls.  d of p is not read. */
+fs_status fs_logprobs(const fs_params* p, const void* logits, int dtype, int64_t ld,
+                      const float* temp, const uint32_t* allow, const int32_t* token,
+                      int32_t n_top, float* out_logprob, int32_t* out_rank, float* out_lse,
+                      float* out_entropy, int32_t* top_idx, float* top_logprob, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/* fs_logprobs_grad -- gradient of fs_logprobs with respect to the logits:
+ *   dl_i = (1 / temp) [ p_i (g_lse - g_logprob - sum_j g_top_j
+ *                            - g_entropy (ln p_i + entropy))
+ *                       + [i = token] g_logprob + sum_j [i = top_idx_j] g_top_j ]
+ * with ln p_i = x_i - lse; 0 for masked ids, and for a whole row whose lse is
+ * not finite.  Sums are FP32, the result is rounded once to `dtype`.
+ *   logits, dtype, ld, temp, allow, token, n_top, top_idx   as given to and
+ *                returned by fs_logprobs (a top_idx of -1, and the g_logprob of
+ *                a negative token, count as absent)
+ *   lse          device float [B]; with a sharded vocabulary the global one
+ *   entropy      device float [B]; needed with g_entropy (else may be NULL)
+ *   g_logprob, g_lse, g_entropy  device float [B], each or NULL (zero)
+ *   g_top        device float [B, n_top] or NULL (zero)
+ *   grad         device, B rows of V elements of type `dtype`, ld_grad >= V
+ *                apart; may be `logits` itself with ld_grad == ld, and no
+ *                other overlap
+ * No workspace; d of p is not read. */
+fs_status fs_logprobs_grad(const fs_params* p, const void* logits, int dtype, int64_t ld,
+                           const float* temp, const uint32_t* allow, const int32_t* token,
+                           int32_t n_top, const int32_t* top_idx, const float* lse,
+                           const float* entropy, const float* g_logprob, const float* g_lse,
+                           const float* g_entropy, const float* g_top, void* grad,
+                           int64_t ld_grad, void* stream);
+
+/* fs_embed -- embedding of p->B token ids: out[n, :] = scale * W[ids[n] -
+ * v_offset, :], computed in FP32 and rounded once; a row of zeros for an id
+ * outside [v_offset, v_offset + V) (-1 from a sample without a valid id, or
+ * another shard's id).
+ *   ids   device int32 [B]; W device [V, d], out device [B, d], both row-major
+ *         of type `dtype`; aligned to their element size, any d; no overlap
+ * n_valid is not read. */
+fs_status fs_embed(const fs_params* p, const int32_t* ids, const void* W, int dtype, float scale,
+                   void* out, void* stream);
+
+/* fs_embed_grad -- gradient of fs_embed with respect to W: dW[v, :] = scale *
+ * sum of g[n, :] over the n with ids[n] - v_offset = v, summed in FP32 in an
+ * order that depends on the ids alone (equal calls give equal bits).
+ *   g           device [B, d] of type `dtype`; aligned to its element size, any d
+ *   dW          device [V, d] of type dw_dtype: `dtype` or FS_F32
+ *   accumulate  0: dW is written whole, with zeros in rows no id names; else
+ *               the sum is added to dW (one rounding) and other rows are left
+ *               as they are
+ * ws: fs_workspace_bytes(p, FS_VARIANT_EMBED_GRAD, 0) bytes, as for
+ * fs_logprobs.  n_valid is not read. */
+fs_status fs_embed_grad(const fs_params* p, const int32_t* ids, const void* g, int dtype,
+                        float scale, int accumulate, void* dW, int dw_dtype, void* ws,
+                        size_t ws_bytes, void* stream);
 
 /* fs_debug_noise -- test export: for rows b0..b0+nb-1 and global ids
  * i0..i0+ni-1 writes the raw Philox words (device uint32 [nb, ni], may be

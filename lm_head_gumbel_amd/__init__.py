@@ -16,7 +16,8 @@ LIB_PATH = os.path.join(PKG, "libfs.so")
 FS_OK, FS_ERR_INVALID_ARG, FS_ERR_UNSUPPORTED, FS_ERR_WORKSPACE, FS_ERR_HIP = range(5)
 FS_NO_NOISE = 1
 (FS_VARIANT_FLAT, FS_VARIANT_GROUPED, FS_VARIANT_TOPK, FS_VARIANT_MULTINOMIAL,
- FS_VARIANT_LOGITS) = range(5)
+ FS_VARIANT_LOGITS, FS_VARIANT_LOGPROBS, FS_VARIANT_EMBED_GRAD) = range(7)
+FS_F32, FS_BF16, FS_F16 = range(3)
 
 
 class fs_params(ctypes.Structure):
@@ -37,6 +38,23 @@ def params(B, d, V, n_valid=None, v_offset=0, tile_v=0, seed=0, step=0, flags=0,
         n_valid = v_offset + V
     return fs_params(B, d, V, n_valid, v_offset, tile_v, seed & 0xFFFFFFFFFFFFFFFF,
                      step & 0xFFFFFFFF, flags, _ptr(seeds), _ptr(step_ptr))
+
+
+class fs_quant(ctypes.Structure):
+    """Mirror of the C struct fs_quant (include/fs.h)."""
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
+
+
+def quant(q, scale, zero, group, scale_dtype=None):
+    """Build an fs_quant from q [V, d / 2] uint8, scale [V, d / group] and zero
+    (uint8 [V, d / group] or None): tensors, which it keeps alive, or raw
+    addresses (then scale_dtype must be given)."""
+    if not _ready(q, scale, zero):
+        raise ValueError("quant: tensors must be contiguous and on the current device")
+    w = fs_quant(_ptr(q), _ptr(scale), _ptr(zero), group, _dtype(scale, scale_dtype))
+    w.tensors = (q, scale, zero)
+    return w
 
 
 class FsError(RuntimeError):
@@ -76,6 +94,19 @@ _SIGS = {
                                  _P]),
     "fs_multinomial": (ctypes.c_int, [ctypes.POINTER(fs_params), _P, _P, _P, _P, _P,
                                       ctypes.c_size_t, _P]),
+    "fs_logits_quant": (ctypes.c_int, [ctypes.POINTER(fs_params), _P, ctypes.POINTER(fs_quant), _P,
+                                       _P]),
+    "fs_logprobs": (ctypes.c_int, [ctypes.POINTER(fs_params), _P, ctypes.c_int, ctypes.c_int64, _P,
+                                   _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P,
+                                   ctypes.c_size_t, _P]),
+    "fs_logprobs_grad": (ctypes.c_int, [ctypes.POINTER(fs_params), _P, ctypes.c_int,
+                                        ctypes.c_int64, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P,
+                                        _P, _P, _P, _P, ctypes.c_int64, _P]),
+    "fs_embed": (ctypes.c_int, [ctypes.POINTER(fs_params), _P, _P, ctypes.c_int, ctypes.c_float,
+                                _P, _P]),
+    "fs_embed_grad": (ctypes.c_int, [ctypes.POINTER(fs_params), _P, _P, ctypes.c_int,
+                                     ctypes.c_float, ctypes.c_int, _P, ctypes.c_int, _P,
+                                     ctypes.c_size_t, _P]),
     "fs_debug_noise": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32,
                                       ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
                                       ctypes.c_int32, _P, _P, _P]),
@@ -120,6 +151,43 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _ready(*xs):
+    """Whether every tensor among xs is contiguous and on the current device
+    (raw addresses and None pass)."""
+    dev = None
+    for x in xs:
+        if x is None or isinstance(x, int):
+            continue
+        if not x.is_cuda or not x.is_contiguous():
+            return False
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device()
+        if x.get_device() != dev:
+            return False
+    return True
+
+
+def _dtype(x, dtype):
+    """The element type of tensor x, or `dtype` where that is given (-1: none)."""
+    if dtype is not None or x is None or isinstance(x, int):
+        return -1 if dtype is None else dtype
+    return {"torch.float32": FS_F32, "torch.bfloat16": FS_BF16, "torch.float16": FS_F16}.get(
+        str(x.dtype), -1)
+
+
+def _rows(x, p, ld):
+    """Row distance in elements of a [B, V] operand whose rows are contiguous
+    (-1: it has no such layout, or is not of p's shape)."""
+    if ld is not None or x is None or isinstance(x, int):
+        return p.V if ld is None else ld
+    if x.dim() != 2 or x.shape[0] != p.B or x.shape[1] != p.V or (p.V > 1 and x.stride(1) != 1):
+        return -1
+    if not _ready(x[:0]):
+        return -1
+    return x.stride(0) if p.B > 1 else max(p.V, x.stride(0))
 
 
 def _ws(ws, ws_bytes):
@@ -216,6 +284,62 @@ def fs_multinomial(p, logits, temp, allow, out_idx, ws=None, ws_bytes=None, stre
     w, n = _ws(ws, ws_bytes)
     return lib().fs_multinomial(ctypes.byref(p), _ptr(logits), _ptr(temp), _ptr(allow),
                                 _ptr(out_idx), w, n, _stream(stream))
+
+
+# The operators below read a tensor's element type and row distance off the
+# tensor; raw addresses need them as arguments.  A tensor that is not
+# contiguous (beyond the row distance), of another element type, or on another
+# device than the current one is FS_ERR_INVALID_ARG.
+
+def fs_logits_quant(p, H, W, logits, stream=None):
+    if not _ready(H, logits):
+        return FS_ERR_INVALID_ARG
+    return lib().fs_logits_quant(ctypes.byref(p), _ptr(H), None if W is None else ctypes.byref(W),
+                                 _ptr(logits), _stream(stream))
+
+
+def fs_logprobs(p, logits, temp, allow, token, n_top, out_logprob=None, out_rank=None,
+                out_lse=None, out_entropy=None, top_idx=None, top_logprob=None, ws=None,
+                ws_bytes=None, stream=None, dtype=None, ld=None):
+    if not _ready(temp, allow, token, out_logprob, out_rank, out_lse, out_entropy, top_idx,
+                  top_logprob, ws):
+        return FS_ERR_INVALID_ARG
+    w, n = _ws(ws, ws_bytes)
+    return lib().fs_logprobs(ctypes.byref(p), _ptr(logits), _dtype(logits, dtype),
+                             _rows(logits, p, ld), _ptr(temp), _ptr(allow), _ptr(token), n_top,
+                             _ptr(out_logprob), _ptr(out_rank), _ptr(out_lse), _ptr(out_entropy),
+                             _ptr(top_idx), _ptr(top_logprob), w, n, _stream(stream))
+
+
+def fs_logprobs_grad(p, logits, temp, allow, token, n_top, top_idx, lse, entropy, g_logprob, g_lse,
+                     g_entropy, g_top, grad, stream=None, dtype=None, ld=None, ld_grad=None):
+    if not _ready(temp, allow, token, top_idx, lse, entropy, g_logprob, g_lse, g_entropy, g_top):
+        return FS_ERR_INVALID_ARG
+    dt = _dtype(logits, dtype)
+    if _dtype(grad, dtype) != dt:
+        return FS_ERR_INVALID_ARG
+    return lib().fs_logprobs_grad(ctypes.byref(p), _ptr(logits), dt, _rows(logits, p, ld),
+                                  _ptr(temp), _ptr(allow), _ptr(token), n_top, _ptr(top_idx),
+                                  _ptr(lse), _ptr(entropy), _ptr(g_logprob), _ptr(g_lse),
+                                  _ptr(g_entropy), _ptr(g_top), _ptr(grad),
+                                  _rows(grad, p, ld_grad), _stream(stream))
+
+
+def fs_embed(p, ids, W, scale, out, stream=None, dtype=None):
+    dt = _dtype(W, dtype)
+    if not _ready(ids, W, out) or _dtype(out, dtype) != dt:
+        return FS_ERR_INVALID_ARG
+    return lib().fs_embed(ctypes.byref(p), _ptr(ids), _ptr(W), dt, scale, _ptr(out),
+                          _stream(stream))
+
+
+def fs_embed_grad(p, ids, g, scale, accumulate, dW, ws=None, ws_bytes=None, stream=None,
+                  dtype=None, dw_dtype=None):
+    if not _ready(ids, g, dW, ws):
+        return FS_ERR_INVALID_ARG
+    w, n = _ws(ws, ws_bytes)
+    return lib().fs_embed_grad(ctypes.byref(p), _ptr(ids), _ptr(g), _dtype(g, dtype), scale,
+                               accumulate, _ptr(dW), _dtype(dW, dw_dtype), w, n, _stream(stream))
 
 
 def fs_debug_noise(seed, step, stream_id, b0, nb, i0, ni, words=None, gumbel=None, stream=None):

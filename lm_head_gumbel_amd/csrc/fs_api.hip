@@ -9,6 +9,7 @@
 
 #include "fs.h"
 #include "fs_internal.h"
+#include "fs_vocab.h"
 
 namespace {
 
@@ -98,6 +99,14 @@ Workspace carve(char* base, const WsLayout& l) {
 }
 
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
+
+// Element size of an element type, 0 for any other number.
+size_t elem_size(int dtype) {
+    return dtype == FS_F32 ? 4 : dtype == FS_BF16 || dtype == FS_F16 ? 2 : 0;
+}
+bool elem_aligned(const void* q, int dtype) {
+    return reinterpret_cast<uintptr_t>(q) % elem_size(dtype) == 0;
+}
 
 fs_status from_hip(hipError_t e) { return e == hipSuccess ? FS_OK : FS_ERR_HIP; }
 
@@ -205,6 +214,12 @@ int32_t fs_num_tiles(const fs_params* p) {
 }
 
 size_t fs_workspace_bytes(const fs_params* p, int variant, int32_t k) {
+    if (variant == FS_VARIANT_LOGPROBS || variant == FS_VARIANT_EMBED_GRAD) {
+        DeviceInfo dev;
+        if (check_params_any_d(p) != FS_OK || !current_device(dev)) return 0;
+        if (variant == FS_VARIANT_LOGPROBS && (k < 0 || k > kMaxAlternatives)) return 0;
+        return kAlign;
+    }
     if (check_params(p) != FS_OK) return 0;
     if (variant < FS_VARIANT_FLAT || variant > FS_VARIANT_LOGITS) return 0;
     if (variant == FS_VARIANT_TOPK && (k < 1 || k > kMaxTopK)) return 0;
@@ -441,6 +456,107 @@ fs_status fs_multinomial(const fs_params* p, const float* logits, const float* t
     return from_hip(launch_multinomial(logits, temp, allow, p->B, p->V, p->n_valid, p->v_offset,
                                        noise_src(pl, p), p->flags, nchunk,
                                        kMultinomialChunk, w.mm, w.ms, w.mkey, out_idx, s));
+}
+
+fs_status fs_logits_quant(const fs_params* p, const void* H, const fs_quant* W, float* logits,
+                          void* stream) {
+    fs_status st = check_params(p);
+    if (st != FS_OK) return st;
+    if (!W || elem_size(W->scale_dtype) == 0 || W->group < 1) return FS_ERR_INVALID_ARG;
+    if (p->B == 0 || p->V == 0) return FS_OK;
+    if (!logits) return FS_ERR_INVALID_ARG;
+    if (W->group != 32 && W->group != 64 && W->group % 128 != 0) return FS_ERR_UNSUPPORTED;
+    if (p->d % W->group != 0) return FS_ERR_UNSUPPORTED;
+    if (p->d > 0 && !W->scale) return FS_ERR_INVALID_ARG;
+    if ((st = check_operands(p, H, W->q)) != FS_OK) return st;
+    if (p->d > 0 && !elem_aligned(W->scale, W->scale_dtype)) return FS_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if (!current_device(dev)) return FS_ERR_UNSUPPORTED;
+    const QuantArgs a{static_cast<const uint16_t*>(H), static_cast<const uint8_t*>(W->q), W->scale,
+                      W->zero, logits, p->B, p->d, p->V, W->group, W->scale_dtype};
+    return from_hip(launch_quant(a, dev.cus, static_cast<hipStream_t>(stream)));
+}
+
+fs_status fs_logprobs(const fs_params* p, const void* logits, int dtype, int64_t ld,
+                      const float* temp, const uint32_t* allow, const int32_t* token,
+                      int32_t n_top, float* out_logprob, int32_t* out_rank, float* out_lse,
+                      float* out_entropy, int32_t* top_idx, float* top_logprob, void* ws,
+                      size_t ws_bytes, void* stream) {
+    const fs_status st = check_params_any_d(p);
+    if (st != FS_OK) return st;
+    if (elem_size(dtype) == 0 || ld < p->V || n_top < 0) return FS_ERR_INVALID_ARG;
+    if (n_top > kMaxAlternatives) return FS_ERR_UNSUPPORTED;
+    if (p->B == 0) return FS_OK;
+    if ((out_logprob || out_rank) && !token) return FS_ERR_INVALID_ARG;
+    if (n_top > 0 && (!top_idx || !top_logprob)) return FS_ERR_INVALID_ARG;
+    if (p->V > 0 && !logits) return FS_ERR_INVALID_ARG;
+    if (p->V > 0 && !elem_aligned(logits, dtype)) return FS_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if (!current_device(dev)) return FS_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < fs_workspace_bytes(p, FS_VARIANT_LOGPROBS, n_top))
+        return FS_ERR_WORKSPACE;
+    const LogprobsArgs a{logits, dtype, ld, temp, allow, token, p->B, p->V, p->n_valid,
+                         p->v_offset, n_top, p->flags, out_logprob, out_rank, out_lse,
+                         out_entropy, top_idx, top_logprob};
+    return from_hip(launch_logprobs(a, ws, static_cast<hipStream_t>(stream)));
+}
+
+fs_status fs_logprobs_grad(const fs_params* p, const void* logits, int dtype, int64_t ld,
+                           const float* temp, const uint32_t* allow, const int32_t* token,
+                           int32_t n_top, const int32_t* top_idx, const float* lse,
+                           const float* entropy, const float* g_logprob, const float* g_lse,
+                           const float* g_entropy, const float* g_top, void* grad,
+                           int64_t ld_grad, void* stream) {
+    const fs_status st = check_params_any_d(p);
+    if (st != FS_OK) return st;
+    if (elem_size(dtype) == 0 || ld < p->V || ld_grad < p->V || n_top < 0)
+        return FS_ERR_INVALID_ARG;
+    if (n_top > kMaxAlternatives) return FS_ERR_UNSUPPORTED;
+    if (p->B == 0 || p->V == 0) return FS_OK;
+    if (!logits || !grad || !lse) return FS_ERR_INVALID_ARG;
+    if (grad == logits && ld_grad != ld) return FS_ERR_INVALID_ARG;
+    if ((g_logprob && !token) || (g_entropy && !entropy)) return FS_ERR_INVALID_ARG;
+    if (n_top > 0 && g_top && !top_idx) return FS_ERR_INVALID_ARG;
+    if (!elem_aligned(logits, dtype) || !elem_aligned(grad, dtype)) return FS_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if (!current_device(dev)) return FS_ERR_UNSUPPORTED;
+    const LogprobsGradArgs a{logits, grad, dtype, ld, ld_grad, temp, allow, token, top_idx, lse,
+                             entropy, g_logprob, g_lse, g_entropy, n_top > 0 ? g_top : nullptr,
+                             p->B, p->V, p->n_valid, p->v_offset, n_top, p->flags};
+    return from_hip(launch_logprobs_grad(a, static_cast<hipStream_t>(stream)));
+}
+
+fs_status fs_embed(const fs_params* p, const int32_t* ids, const void* W, int dtype, float scale,
+                   void* out, void* stream) {
+    const fs_status st = check_params_any_d(p);
+    if (st != FS_OK) return st;
+    if (elem_size(dtype) == 0) return FS_ERR_INVALID_ARG;
+    if (p->B == 0 || p->d == 0) return FS_OK;
+    if (!ids || !out || (p->V > 0 && !W)) return FS_ERR_INVALID_ARG;
+    if (!elem_aligned(out, dtype) || !elem_aligned(W, dtype)) return FS_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if (!current_device(dev)) return FS_ERR_UNSUPPORTED;
+    const EmbedArgs a{ids, W, out, p->B, p->d, p->V, p->v_offset, dtype, scale};
+    return from_hip(launch_embed(a, static_cast<hipStream_t>(stream)));
+}
+
+fs_status fs_embed_grad(const fs_params* p, const int32_t* ids, const void* g, int dtype,
+                        float scale, int accumulate, void* dW, int dw_dtype, void* ws,
+                        size_t ws_bytes, void* stream) {
+    const fs_status st = check_params_any_d(p);
+    if (st != FS_OK) return st;
+    if (elem_size(dtype) == 0 || elem_size(dw_dtype) == 0) return FS_ERR_INVALID_ARG;
+    if (dw_dtype != dtype && dw_dtype != FS_F32) return FS_ERR_UNSUPPORTED;
+    if (p->d == 0 || p->V == 0 || (p->B == 0 && accumulate)) return FS_OK;
+    if (!dW || (p->B > 0 && (!ids || !g))) return FS_ERR_INVALID_ARG;
+    if (!elem_aligned(g, dtype) || !elem_aligned(dW, dw_dtype)) return FS_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if (!current_device(dev)) return FS_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < fs_workspace_bytes(p, FS_VARIANT_EMBED_GRAD, 0))
+        return FS_ERR_WORKSPACE;
+    const EmbedGradArgs a{ids, g, dW, p->B, p->d, p->V, p->v_offset, dtype, dw_dtype, scale,
+                          accumulate};
+    return from_hip(launch_embed_grad(a, ws, static_cast<hipStream_t>(stream)));
 }
 
 fs_status fs_debug_noise(uint64_t seed, uint32_t step, uint32_t stream_id, int32_t b0,

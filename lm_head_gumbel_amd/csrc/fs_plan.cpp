@@ -75,18 +75,22 @@ ResidentConfig resident_default(int nb, int nks, int variant) {
 
 int resident_topk_rows(const ResidentConfig& c) { return topk_store_rows(c.nb, c.hl); }
 
-fs_status check_params(const fs_params* p) {
+static fs_status check(const fs_params* p, int d_step) {
     if (!p) return FS_ERR_INVALID_ARG;
     if (p->B < 0 || p->d < 0 || p->V < 0 || p->v_offset < 0 || p->tile_v < 0)
         return FS_ERR_INVALID_ARG;
     if (p->B > kMaxB) return FS_ERR_UNSUPPORTED;
     if ((int64_t)p->v_offset + p->V > INT32_MAX) return FS_ERR_INVALID_ARG;
-    if (p->d % 8 != 0) return FS_ERR_UNSUPPORTED;
+    if (p->d % d_step != 0) return FS_ERR_UNSUPPORTED;
     if (p->v_offset % kMBlock != 0) return FS_ERR_UNSUPPORTED;
     if (p->tile_v % kMBlock != 0) return FS_ERR_UNSUPPORTED;
     if (p->flags & ~kFlagNoNoise) return FS_ERR_INVALID_ARG;
     return FS_OK;
 }
+
+fs_status check_params(const fs_params* p) { return check(p, 8); }
+
+fs_status check_params_any_d(const fs_params* p) { return check(p, 1); }
 
 void make_plan(const fs_params* p, int variant, int cus, Plan& pl) {
     cus = std::max(1, cus);
