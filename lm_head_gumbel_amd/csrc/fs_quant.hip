@@ -28,7 +28,6 @@ constexpr int kQWaves = 8;
 constexpr int kQThreads = 64 * kQWaves;
 constexpr int kQBlock = 128;   // k of one load instruction
 constexpr int kQDepth = 4;     // loads of a row block in flight per wave
-constexpr int kQRows = 2;      // row blocks per wave and pass
 
 // Blocks of k whose scales a wave holds in LDS: all kQDepth, or half of them
 // where several column blocks and groups of 32 leave no room for more.
@@ -42,6 +41,7 @@ struct QuantPlan {
     int nkb;       // k blocks of 128, padded to a multiple of kQDepth ksplit
     int KC;        // k blocks per LDS chunk
     int nchunks;
+    int mr;        // 16-row blocks per wave and pass
     int ksplit;    // waves that share a row block (resident only)
     bool chunked;  // H passes through LDS in chunks (else it stays there whole)
     int G;         // workgroups along V
@@ -146,8 +146,8 @@ __device__ __forceinline__ void load_bytes(uint32_t* dst, const char* p) {
     }
 }
 
-template <int NB, int SUB, int ST, bool CHUNKED>
-__global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_kernel(QuantArgs a,
+template <int NB, int MR, int SUB, int ST, bool CHUNKED>
+__global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
                                                                            QuantPlan pl,
                                                                            int group_blocks) {
     extern __shared__ __align__(16) char smem[];
@@ -160,43 +160,40 @@ __global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_
     const int ng = a.d / a.group;
     const int nks = a.d / 8;   // pieces of 8 k
     const int nmb = (a.V + 15) / 16;
-    const int b0 = part_begin(blockIdx.x, nmb, pl.G), b1 = part_begin(blockIdx.x + 1, nmb, pl.G);
     const int RW = kQWaves / pl.ksplit, rw = wave / pl.ksplit, kw = wave % pl.ksplit;
-    // balanced passes over the workgroup's blocks, at most RW kQRows each
-    const int npass = (b1 - b0 + RW * kQRows - 1) / (RW * kQRows);
-    const int pass_len = (b1 - b0) / npass, pass_more = (b1 - b0) % npass;
-    auto pass_begin = [&](int pass) { return b0 + pass * pass_len + min(pass, pass_more); };
+    // pass p of all workgroups sweeps one region of W: blocks p G RW MR ..
+    const int per_pass = RW * MR;
+    const int ntile = (nmb + per_pass - 1) / per_pass;
+    const int npass = (ntile - (int)blockIdx.x + pl.G - 1) / pl.G;
+    auto pass_begin = [&](int pass) { return ((int)blockIdx.x + pass * pl.G) * per_pass; };
 
     // this wave's k blocks of every pass
     const int kper = pl.nkb / pl.ksplit;
     const int kfirst = kw * kper;
     const bool has_zero = a.zero != nullptr;
     const int row_bytes = a.d / 2;
-    // without zero points, bytes of the scales are read and not used
-    const char* zp = has_zero ? reinterpret_cast<const char*>(a.zero)
-                              : static_cast<const char*>(a.scale);
+    const char* zp = reinterpret_cast<const char*>(a.zero);
 
     // ---- W loader: k blocks of a pass in order, kQDepth of them ahead, two
     // at a time (a row's two neighbours share a 128-byte line)
     int ld_pass = 0, ld_k = 0;
-    const char* qrow[kQRows];
+    const char* qrow[MR];
     auto row_of = [&](int pass, int m, int r) {
-        // blocks past the pass re-read its last one, rows past V row V - 1
-        // (cache hits; not stored)
-        return min(min(pass_begin(pass) + m * RW + rw, pass_begin(pass + 1) - 1) * 16 + r, a.V - 1);
+        // rows past V re-read row V - 1 (not stored)
+        return min((pass_begin(pass) + rw * MR + m) * 16 + r, a.V - 1);
     };
     auto rows_of = [&](int pass) {
 #pragma unroll
-        for (int m = 0; m < kQRows; ++m)
+        for (int m = 0; m < MR; ++m)
             qrow[m] = reinterpret_cast<const char*>(a.q) +
                       (size_t)row_of(pass, m, r16) * row_bytes;
     };
-    u32x4 w[kQDepth][kQRows];
-    auto load = [&](u32x4 (&d0)[kQRows], u32x4 (&d1)[kQRows]) __attribute__((always_inline)) {
+    u32x4 w[kQDepth][MR];
+    auto load = [&](u32x4 (&d0)[MR], u32x4 (&d1)[MR]) __attribute__((always_inline)) {
         const int o0 = (kfirst + ld_k) * 64 + q * 16;
         const int c0 = min(o0, row_bytes - 16), c1 = min(o0 + 64, row_bytes - 16);
 #pragma unroll
-        for (int m = 0; m < kQRows; ++m) {
+        for (int m = 0; m < MR; ++m) {
             d0[m] = __builtin_nontemporal_load((const global_u32x4*)(qrow[m] + c0));
             d1[m] = __builtin_nontemporal_load((const global_u32x4*)(qrow[m] + c1));
         }
@@ -214,18 +211,19 @@ __global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_
     constexpr int kSlots = pair_slots(NB, NS);
     const int srow = lane >> 2, skb = lane & 3;
     float2* const pairs = reinterpret_cast<float2*>(smem + pl.pair_off) +
-                          wave * (kQRows * kSlots * NS * 16);
+                          wave * (MR * kSlots * NS * 16);
     int sc_pass = 0, sc_k = 0;
-    Groups<NS, ST> graw[kQRows];
+    Groups<NS, ST> graw[MR];
     auto load_scales = [&]() __attribute__((always_inline)) {
         const int kb = kfirst + sc_k + skb;
         // where the row ends inside the block, the row's last NS groups
         const int i = min(SUB == 4 ? kb / group_blocks : kb * NS, ng - NS);
 #pragma unroll
-        for (int m = 0; m < kQRows; ++m) {
+        for (int m = 0; m < MR; ++m) {
             const size_t at = (size_t)row_of(sc_pass, m, srow) * ng + i;
             load_bytes<NS * SB>(graw[m].s, static_cast<const char*>(a.scale) + at * SB);
-            load_bytes<NS>(&graw[m].z, zp + at);
+            graw[m].z = 0x08080808u;
+            if (has_zero) load_bytes<NS>(&graw[m].z, zp + at);
         }
     };
     // (of the blocks from..from + kSlots - 1 of the kQDepth)
@@ -234,14 +232,14 @@ __global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_
         const int slot = skb - from;
         if (kSlots == kQDepth || (slot >= 0 && slot < kSlots)) {
 #pragma unroll
-        for (int m = 0; m < kQRows; ++m) {
+        for (int m = 0; m < MR; ++m) {
             if constexpr (NS > 1)
                 if (sh > 0 && sh < NS) end_groups(graw[m], sh);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
                 pairs[((m * kSlots + slot) * NS + n) * 16 + srow] =
                     make_float2(group_scale(graw[m], n),
-                                has_zero ? -16.f - (float)((graw[m].z >> (8 * n)) & 0xFFu) : -24.f);
+                                -16.f - (float)((graw[m].z >> (8 * n)) & 0xFFu));
         }
         }
         if (from + kSlots < kQDepth) return;
@@ -289,7 +287,7 @@ __global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_
         }
     };
 
-    f32x4 total[kQRows][NB];
+    f32x4 total[MR][NB];
     // LDS offsets of this lane: its operand piece (columns past the stored
     // ones read the last: their results are not stored) and its sums.  One
     // block of k is at kb * 256 C, and kb * 64 NB NS.
@@ -301,19 +299,31 @@ __global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_
     uint32_t nib_mask = 0x00780078u, sixteen = 0x41804180u;
     asm volatile("" : "+s"(nib_mask), "+v"(sixteen));
     auto consume = [&](int buf, int kb_lds, int slot,
-                       const u32x4 (&wv)[kQRows]) __attribute__((always_inline)) {
-        u32x4 wt[kQRows];
+                       const u32x4 (&wv)[MR]) __attribute__((always_inline)) {
+        u32x4 wt[MR];
 #pragma unroll
-        for (int m = 0; m < kQRows; ++m) wt[m] = transpose_words<SUB>(wv[m]);
+        for (int m = 0; m < MR; ++m) wt[m] = transpose_words<SUB>(wv[m]);
         uint32_t frag = buf + frag0 + kb_lds * 4 * frag_step;
         uint32_t sums = buf + sums0 + kb_lds * (64 * NB * NS);
         asm volatile("" : "+v"(frag), "+v"(sums));   // one address each, formed here
+        // operands of H: all four steps read ahead for one column block, else
+        // one step ahead
+        constexpr int kAhead = NB == 1 ? 4 : 2;
+        bf16x8 hf[kAhead][NB];
+        auto read_h = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+                hf[j % kAhead][c] =
+                    *reinterpret_cast<const bf16x8*>(smem + frag + j * frag_step + c * 256);
+        };
+#pragma unroll
+        for (int j = 0; j < kAhead - (NB == 1 ? 0 : 1); ++j) read_h(j);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            f32x4 acc[kQRows][NB];
-            float s[kQRows], off[kQRows];
+            f32x4 acc[MR][NB];
+            float s[MR], off[MR];
 #pragma unroll
-            for (int m = 0; m < kQRows; ++m) {
+            for (int m = 0; m < MR; ++m) {
                 const float2 v = pairs[((m * kSlots + slot) * NS + n) * 16 + r16];
                 s[m] = v.x;
                 off[m] = v.y;
@@ -322,28 +332,25 @@ __global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_
             for (int c = 0; c < NB; ++c) {
                 const f32x4 h = *reinterpret_cast<const f32x4*>(smem + sums + (n * NB + c) * 64);
 #pragma unroll
-                for (int m = 0; m < kQRows; ++m) acc[m][c] = h * off[m];
+                for (int m = 0; m < MR; ++m) acc[m][c] = h * off[m];
             }
 #pragma unroll
             for (int jj = 0; jj < SUB; ++jj) {
                 const int j = n * SUB + jj;
-                bf16x8 wf[kQRows];
+                if (NB > 1 && j + 1 < 4) read_h(j + 1);
+                bf16x8 wf[MR];
 #pragma unroll
-                for (int m = 0; m < kQRows; ++m) wf[m] = unpack_word(wt[m][j], nib_mask, sixteen);
+                for (int m = 0; m < MR; ++m) wf[m] = unpack_word(wt[m][j], nib_mask, sixteen);
 #pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                    const bf16x8 hf = *reinterpret_cast<const bf16x8*>(smem + frag + j * frag_step +
-                                                                       c * 256);
+                for (int c = 0; c < NB; ++c)
 #pragma unroll
-                    for (int m = 0; m < kQRows; ++m)
-                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf, wf[m], acc[m][c], 0,
-                                                                            0, 0);
-                }
-                if constexpr (NS == 1)
-                    if (jj % 2) __builtin_amdgcn_sched_barrier(0);
+                    for (int m = 0; m < MR; ++m)
+                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            hf[j % kAhead][c], wf[m], acc[m][c], 0, 0, 0);
+                if (NB > 1) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int m = 0; m < kQRows; ++m)
+            for (int m = 0; m < MR; ++m)
 #pragma unroll
                 for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -376,17 +383,16 @@ __global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_
     };
     auto clear = [&]() {
 #pragma unroll
-        for (int m = 0; m < kQRows; ++m)
+        for (int m = 0; m < MR; ++m)
 #pragma unroll
             for (int c = 0; c < NB; ++c) total[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
     auto store = [&](int pass) {
-        const int s = pass_begin(pass), e = pass_begin(pass + 1);
+        const int s = pass_begin(pass) + rw * MR;
 #pragma unroll
-        for (int m = 0; m < kQRows; ++m) {
-            const int blk = s + m * RW + rw;
-            const int row = blk * 16 + r16;
-            if (blk >= e || row >= a.V) continue;
+        for (int m = 0; m < MR; ++m) {
+            const int row = (s + m) * 16 + r16;
+            if (row >= a.V) continue;
 #pragma unroll
             for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -410,29 +416,34 @@ __global__ __launch_bounds__(kQThreads, NB == 1 && !CHUNKED ? 4 : 2) void quant_
     __syncthreads();
 
     if constexpr (!CHUNKED) {
-        float* red = reinterpret_cast<float*>(smem + pl.h_bytes + pl.s_bytes);
+        // ksplit > 1: the totals of a row block's waves meet in LDS, in the
+        // order of k; each wave adds up and stores its share of the MR NB
+        // (row block, column block) tiles.  Two areas, so that one barrier a
+        // pass is enough.
+        f32x4* red = reinterpret_cast<f32x4*>(smem + pl.h_bytes + pl.s_bytes);
         for (int pass = 0; pass < npass; ++pass) {
             clear();
             for (int k = kfirst; k < kfirst + kper; k += kQDepth) sweep(0, k);
-            if (pl.ksplit > 1) {
-                // the waves of a row block meet in the order of k
-                constexpr int kVals = kQRows * NB * 4;
-                if (kw > 0)
-#pragma unroll
-                    for (int v = 0; v < kVals; ++v)
-                        red[(wave * kVals + v) * 64 + lane] = total[v / (4 * NB)][v / 4 % NB][v % 4];
-                __syncthreads();
-                if (kw == 0) {
-                    for (int o = 1; o < pl.ksplit; ++o)
-#pragma unroll
-                        for (int v = 0; v < kVals; ++v)
-                            total[v / (4 * NB)][v / 4 % NB][v % 4] +=
-                                red[((wave + o) * kVals + v) * 64 + lane];
-                    store(pass);
-                }
-                __syncthreads();
-            } else {
+            if (pl.ksplit == 1) {
                 store(pass);
+                continue;
+            }
+            f32x4* area = red + (pass & 1) * (kQWaves * MR * NB * 64);
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+                    area[((m * NB + c) * kQWaves + wave) * 64 + lane] = total[m][c];
+            __syncthreads();
+            const float* sums = reinterpret_cast<const float*>(area);
+            for (int v = kw; v < MR * NB * 4; v += pl.ksplit) {   // value v % 4 of tile v / 4
+                const int t = v >> 2, i = v & 3;
+                const float* at = sums + ((t * kQWaves + rw * pl.ksplit) * 64 + lane) * 4 + i;
+                float sum = at[0];
+                for (int o = 1; o < pl.ksplit; ++o) sum += at[o * 256];
+                const int row = (pass_begin(pass) + rw * MR + t / NB) * 16 + r16;
+                const int b = col0 + t % NB * 16 + q * 4 + i;
+                if (row < a.V && b < a.B) a.logits[(size_t)b * a.V + row] = sum;
             }
         }
     } else {
@@ -477,60 +488,70 @@ QuantPlan quant_plan(const QuantArgs& a, int cus) {
         return p.h_bytes + p.s_bytes;
     };
     p.C = p.nb == 1 ? a.B : 16 * p.nb;
+    // waves along k: as many as have kQDepth blocks each.  Rows lie d / 2
+    // bytes apart, so the waves that share them read longer runs of fewer
+    // rows
     p.ksplit = 1;
-    const size_t red = (size_t)kQWaves * kQRows * p.nb * 4 * 64 * 4;
-    const size_t pairs = (size_t)kQWaves * kQRows * pair_slots(p.nb, ns) * ns * 16 * 8;
-    const size_t all = bytes(round_up(nkb, 8 * kQDepth)) + pairs + red;   // at most this much
-    p.chunked = p.nb == 4 || all > kQLds;
-    if (p.chunked && p.nb == 1) p.nb = 2;   // (chunks are built for two blocks or four)
-    p.grid_y = (a.B + 16 * p.nb - 1) / (16 * p.nb);
+    while (p.ksplit < kQWaves && 2 * p.ksplit * kQDepth <= nkb) p.ksplit *= 2;
+    p.nkb = round_up(nkb, kQDepth * p.ksplit);
+    auto rest = [&](int mr) {   // scales, totals
+        return (size_t)kQWaves * mr * (pair_slots(p.nb, ns) * ns * 16 * 8) +
+               (p.ksplit > 1 ? (size_t)2 * kQWaves * mr * p.nb * 64 * 16 : 0);
+    };
+    p.mr = 2;
+    while (p.mr > 1 && (nmb + p.mr - 1) / p.mr < cus * (kQWaves / p.ksplit)) p.mr /= 2;
+    while (p.mr > 1 && bytes(p.nkb) + rest(p.mr) > kQLds) p.mr /= 2;
+    p.chunked = p.nb == 4 || bytes(p.nkb) + rest(p.mr) > kQLds;
     if (!p.chunked) {
-        const int occ = p.nb == 1 && 2 * all <= kQLds ? 2 : 1;
-        p.G = nmb < cus * occ ? nmb : cus * occ;
-        const int bw = (nmb + p.G - 1) / p.G;   // row blocks of a workgroup
-        while (p.ksplit < 8 && (kQWaves / p.ksplit) * kQRows > bw &&
-               2 * p.ksplit * kQDepth <= nkb)
-            p.ksplit *= 2;
-        p.nkb = round_up(nkb, kQDepth * p.ksplit);
         p.KC = p.nkb;
         p.nchunks = 1;
-        p.pair_off = bytes(p.KC) + (p.ksplit > 1 ? red : 0);
+        p.pair_off = bytes(p.KC) + rest(p.mr) - (size_t)kQWaves * p.mr * (pair_slots(p.nb, ns) * ns * 16 * 8);
+        p.lds = bytes(p.KC) + rest(p.mr);
+        int occ = (int)(kQLds / p.lds);
+        if (occ > 2) occ = 2;
+        const int ntile = (nmb + (kQWaves / p.ksplit) * p.mr - 1) / ((kQWaves / p.ksplit) * p.mr);
+        p.G = ntile < cus * occ ? ntile : cus * occ;
     } else {
+        if (p.nb == 1) p.nb = 2;   // (chunks are built for two column blocks or four)
         p.C = 16 * p.nb;
+        p.ksplit = 1;
+        p.mr = 2;
         p.KC = 2 * kQWaves / p.nb / kQDepth * kQDepth;
         p.nkb = round_up(nkb, p.KC);
         p.nchunks = p.nkb / p.KC;
-        p.G = nmb < cus ? nmb : cus;
         p.pair_off = (p.nchunks == 1 ? 1 : 2) * bytes(p.KC);
+        p.lds = p.pair_off + rest(p.mr);   // at most 152 KiB (group 32)
+        const int ntile = (nmb + kQWaves * p.mr - 1) / (kQWaves * p.mr);
+        p.G = ntile < cus ? ntile : cus;
     }
-    p.lds = p.pair_off + pairs;   // chunked: at most 152 KiB (group 32)
+    p.grid_y = (a.B + 16 * p.nb - 1) / (16 * p.nb);
     return p;
 }
 
-template <int NB, int SUB, int ST, bool CHUNKED>
+template <int NB, int MR, int SUB, int ST, bool CHUNKED>
 hipError_t launch(const QuantArgs& a, const QuantPlan& p, hipStream_t stream) {
     const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&quant_kernel<NB, SUB, ST, CHUNKED>),
+        hipFuncSetAttribute(reinterpret_cast<const void*>(&quant_kernel<NB, MR, SUB, ST, CHUNKED>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)kQLds);
     if (e != hipSuccess) return e;
     const int group_blocks = a.group >= kQBlock ? a.group / kQBlock : 1;
-    hipLaunchKernelGGL((quant_kernel<NB, SUB, ST, CHUNKED>), dim3(p.G, p.grid_y), dim3(kQThreads),
+    hipLaunchKernelGGL((quant_kernel<NB, MR, SUB, ST, CHUNKED>), dim3(p.G, p.grid_y), dim3(kQThreads),
                        p.lds, stream, a, p, group_blocks);
     return hipGetLastError();
 }
 
-template <int NB, int ST, bool CHUNKED>
+template <int NB, int MR, int ST, bool CHUNKED>
 hipError_t launch_sub(const QuantArgs& a, const QuantPlan& p, hipStream_t stream) {
-    return a.group == 32   ? launch<NB, 1, ST, CHUNKED>(a, p, stream)
-           : a.group == 64 ? launch<NB, 2, ST, CHUNKED>(a, p, stream)
-                           : launch<NB, 4, ST, CHUNKED>(a, p, stream);
+    return a.group == 32   ? launch<NB, MR, 1, ST, CHUNKED>(a, p, stream)
+           : a.group == 64 ? launch<NB, MR, 2, ST, CHUNKED>(a, p, stream)
+                           : launch<NB, MR, 4, ST, CHUNKED>(a, p, stream);
 }
 
-template <int NB, bool CHUNKED>
+template <int NB, int MR, bool CHUNKED>
 hipError_t launch_nb(const QuantArgs& a, const QuantPlan& p, hipStream_t stream) {
-    return a.scale_dtype == FS_F32    ? launch_sub<NB, FS_F32, CHUNKED>(a, p, stream)
-           : a.scale_dtype == FS_BF16 ? launch_sub<NB, FS_BF16, CHUNKED>(a, p, stream)
-                                      : launch_sub<NB, FS_F16, CHUNKED>(a, p, stream);
+    return a.scale_dtype == FS_F32    ? launch_sub<NB, MR, FS_F32, CHUNKED>(a, p, stream)
+           : a.scale_dtype == FS_BF16 ? launch_sub<NB, MR, FS_BF16, CHUNKED>(a, p, stream)
+                                      : launch_sub<NB, MR, FS_F16, CHUNKED>(a, p, stream);
 }
 
 // d below one block of 128: one thread per logit, w = s (q - z) in FP32.
@@ -570,9 +591,13 @@ hipError_t launch_quant(const QuantArgs& a, int cus, hipStream_t stream) {
         return hipGetLastError();
     }
     const QuantPlan p = quant_plan(a, cus);
-    if (p.nb == 1) return launch_nb<1, false>(a, p, stream);
-    if (p.nb == 2) return p.chunked ? launch_nb<2, true>(a, p, stream) : launch_nb<2, false>(a, p, stream);
-    return launch_nb<4, true>(a, p, stream);
+    if (p.nb == 1)
+        return p.mr == 2 ? launch_nb<1, 2, false>(a, p, stream)
+                         : launch_nb<1, 1, false>(a, p, stream);
+    if (p.chunked)
+        return p.nb == 2 ? launch_nb<2, 2, true>(a, p, stream)
+                         : launch_nb<4, 2, true>(a, p, stream);
+    return p.mr == 2 ? launch_nb<2, 2, false>(a, p, stream) : launch_nb<2, 1, false>(a, p, stream);
 }
 
 }  // namespace fs
