@@ -268,7 +268,7 @@ typedef struct {
     const void* q;        /* device [V, d / 2] bytes, 16-byte aligned: byte i of a row
                              holds q[j, 2i] in its low and q[j, 2i + 1] in its high
                              four bits, each 0..15                               */
-    const void* scale;    /* device [V, d / group] of scale_dtype                */
+    const void* scale;    /* device [V, d / group] of scale_dtype, finite        */
     const uint8_t* zero;  /* device [V, d / group], or NULL: 8 everywhere        */
     int32_t group;        /* consecutive k that share a scale: 32, 64, or a
                              multiple of 128; divides d                          */
@@ -308,8 +308,9 @@ fs_status fs_logits_quant(const fs_params* p, const void* H, const fs_quant* W, 
  * alternative.  Shards of one vocabulary (v_offset): with L = logaddexp of the
  * shards' lse, a global ln p is the shard's ln p + lse - L, the global entropy
  * the sum over shards of w (entropy + L - lse), w = exp(lse - L).
- * ws: fs_workspace_bytes(p, FS_VARIANT_LOGPROBS, n_top) bytes; it needs no
- * initialisation and keeps nothing between calls.  d of p is not read. */
+ * ws: fs_workspace_bytes(p, FS_VARIANT_LOGPROBS, n_top) bytes, 16-byte
+ * aligned; it needs no initialisation and keeps nothing between calls.  d of p
+ * is not read.  V above 2^31 - 65537 is FS_ERR_UNSUPPORTED. */
 fs_status fs_logprobs(const fs_params* p, const void* logits, int dtype, int64_t ld,
                       const float* temp, const uint32_t* allow, const int32_t* token,
                       int32_t n_top, float* out_logprob, int32_t* out_rank, float* out_lse,

@@ -217,8 +217,9 @@ size_t fs_workspace_bytes(const fs_params* p, int variant, int32_t k) {
     if (variant == FS_VARIANT_LOGPROBS || variant == FS_VARIANT_EMBED_GRAD) {
         DeviceInfo dev;
         if (check_params_any_d(p) != FS_OK || !current_device(dev)) return 0;
-        if (variant == FS_VARIANT_LOGPROBS && (k < 0 || k > kMaxAlternatives)) return 0;
-        return kAlign;
+        if (variant == FS_VARIANT_EMBED_GRAD) return kAlign;
+        if (k < 0 || k > kMaxAlternatives || p->V > kMaxRow) return 0;
+        return std::max(kAlign, logprobs_ws_bytes(p->B, p->V, k, dev.cus));
     }
     if (check_params(p) != FS_OK) return 0;
     if (variant < FS_VARIANT_FLAT || variant > FS_VARIANT_LOGITS) return 0;
@@ -485,7 +486,7 @@ fs_status fs_logprobs(const fs_params* p, const void* logits, int dtype, int64_t
     const fs_status st = check_params_any_d(p);
     if (st != FS_OK) return st;
     if (elem_size(dtype) == 0 || ld < p->V || n_top < 0) return FS_ERR_INVALID_ARG;
-    if (n_top > kMaxAlternatives) return FS_ERR_UNSUPPORTED;
+    if (n_top > kMaxAlternatives || p->V > kMaxRow) return FS_ERR_UNSUPPORTED;
     if (p->B == 0) return FS_OK;
     if ((out_logprob || out_rank) && !token) return FS_ERR_INVALID_ARG;
     if (n_top > 0 && (!top_idx || !top_logprob)) return FS_ERR_INVALID_ARG;
@@ -493,12 +494,13 @@ fs_status fs_logprobs(const fs_params* p, const void* logits, int dtype, int64_t
     if (p->V > 0 && !elem_aligned(logits, dtype)) return FS_ERR_UNSUPPORTED;
     DeviceInfo dev;
     if (!current_device(dev)) return FS_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < fs_workspace_bytes(p, FS_VARIANT_LOGPROBS, n_top))
+    if (!ws || ws_bytes < std::max(kAlign, logprobs_ws_bytes(p->B, p->V, n_top, dev.cus)))
         return FS_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) % 16 != 0) return FS_ERR_UNSUPPORTED;
     const LogprobsArgs a{logits, dtype, ld, temp, allow, token, p->B, p->V, p->n_valid,
                          p->v_offset, n_top, p->flags, out_logprob, out_rank, out_lse,
                          out_entropy, top_idx, top_logprob};
-    return from_hip(launch_logprobs(a, ws, static_cast<hipStream_t>(stream)));
+    return from_hip(launch_logprobs(a, ws, dev.cus, static_cast<hipStream_t>(stream)));
 }
 
 fs_status fs_logprobs_grad(const fs_params* p, const void* logits, int dtype, int64_t ld,
@@ -511,7 +513,7 @@ fs_status fs_logprobs_grad(const fs_params* p, const void* logits, int dtype, in
     if (st != FS_OK) return st;
     if (elem_size(dtype) == 0 || ld < p->V || ld_grad < p->V || n_top < 0)
         return FS_ERR_INVALID_ARG;
-    if (n_top > kMaxAlternatives) return FS_ERR_UNSUPPORTED;
+    if (n_top > kMaxAlternatives || p->V > kMaxRow) return FS_ERR_UNSUPPORTED;
     if (p->B == 0 || p->V == 0) return FS_OK;
     if (!logits || !grad || !lse) return FS_ERR_INVALID_ARG;
     if (grad == logits && ld_grad != ld) return FS_ERR_INVALID_ARG;

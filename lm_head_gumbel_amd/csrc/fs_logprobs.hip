@@ -1,151 +1,687 @@
-// Log probabilities of materialised logits: a given token's, the row's
-// log-sum-exp and entropy, the best alternatives; and their gradient.
+// Log probabilities of materialised logits: a given token's and its rank, the
+// row's log-sum-exp and entropy, the best alternatives; and their gradient.
 //
-// With m = max l, S = sum exp((l - m)/T) and A = sum (l - m)/T exp((l - m)/T)
-// over the unmasked ids of a row:  lse = m/T + ln S,  log p_i = (l_i - m)/T -
-// ln S,  entropy = ln S - A/S.
+// With m = max l, x_i = (l_i - m) / T, S = sum e^{x_i} and A = sum x_i e^{x_i}
+// over the unmasked ids of a row:  lse = m / T + ln S,  ln p_i = x_i - ln S,
+// entropy = ln S - A / S.  (m, S, A) of disjoint slices join: with M the
+// larger m and w = e^{(m - M) / T}, S adds w S and A adds w (A + (m - M) / T S).
+//
+// Bound by the one read of the logits.  A workgroup takes a slice of a row
+// into registers (E elements a thread, all loads issued before the first
+// use), so the slice's maximum is known before the first exponential and no
+// running sum is ever rescaled; a second kernel joins the slices of a row.
+#include <algorithm>
+#include <type_traits>
+
 #include "fs_vocab.h"
 
 namespace fs {
 
+namespace {
+
 constexpr int kLpThreads = 256;
+constexpr int kLpWaves = kLpThreads / 64;
+constexpr int kLpShort = 8;    // elements per thread of a short slice
+constexpr int kLpLong = 32;    // and of a long one
+constexpr int kHeads = 1024;   // slices whose first entries the join keeps in LDS
+constexpr int kCandidates = kMaxAlternatives * kLpLong;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kFloor = -1e30f;   // exponents: e^{-inf} without inf * 0
 
+// 16 bytes of elements as they lie in memory, four 32-bit words.
 template <int DT>
-__device__ __forceinline__ float row_logit(const void* row, const uint32_t* allow_row, int i) {
-    const float l = (float)static_cast<const typename Elem<DT>::type*>(row)[i];
-    return allowed(allow_row, i) ? clean_logit(l) : -INFINITY;
-}
-
-template <typename F, typename V>
-__device__ V block_reduce(V v, V* slot, F op) {
-    __syncthreads();
-    slot[threadIdx.x] = v;
-    __syncthreads();
-    for (int s = kLpThreads / 2; s >= 1; s >>= 1) {
-        if (threadIdx.x < s) slot[threadIdx.x] = op(slot[threadIdx.x], slot[threadIdx.x + s]);
-        __syncthreads();
+struct Vec {
+    typedef typename Elem<DT>::type E;
+    static constexpr int kN = 16 / (int)sizeof(E);   // elements
+    uint32_t w[4];
+    // element e in FP32
+    __device__ __forceinline__ float at(int e) const {
+        if constexpr (DT == FS_F32) return __uint_as_float(w[e]);
+        const uint32_t h = e % 2 ? w[e / 2] >> 16 : w[e / 2];
+        return DT == FS_BF16 ? __uint_as_float(h << 16)
+                             : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
     }
-    return slot[0];
+};
+// -inf in both halves (or the whole) of a word.
+template <int DT>
+constexpr uint32_t kMinusInf = DT == FS_F32 ? 0xFF800000u : DT == FS_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+
+// Ids of the row that can be unmasked.
+__device__ __forceinline__ int valid_ids(int V, int n_valid, int v_offset) {
+    return (int)min((int64_t)V, max((int64_t)0, (int64_t)n_valid - v_offset));
 }
 
+// FP32 logit: NaN -> -inf, +inf -> the largest finite value.
+__device__ __forceinline__ float clean(float l) {
+    return fminf(l == l ? l : -INFINITY, 3.402823466e38f);
+}
+
+// Bit o of the result: id i + o is allowed (o < n <= 8; i + n <= V).
+__device__ __forceinline__ uint32_t allow_bits(const uint32_t* row, int i, int n) {
+    const uint32_t lo = row[i >> 5], hi = row[(i + n - 1) >> 5];
+    const int sh = i & 31;
+    return sh + n > 32 ? (lo >> sh) | (hi << (32 - sh)) : lo >> sh;
+}
+
+// A wave's chunk of 64 kN consecutive ids of a row: whole inside the row, a
+// lane holds kN consecutive ids from one 16-byte load (at any alignment of
+// the row to its element size); where the row ends inside, lane l holds ids
+// l, l + 64, ..  Everything here but the lane is the same for the whole wave.
 template <int DT>
-__global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
-    __shared__ float fslot[kLpThreads];
-    __shared__ int islot[kLpThreads];
-    __shared__ uint64_t kslot[kLpThreads];
-    const int Vv = min((int64_t)a.V, max((int64_t)0, (int64_t)a.n_valid - a.v_offset));
-    auto add = [](float x, float y) { return x + y; };
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const void* row =
-            static_cast<const char*>(a.logits) + (size_t)b * a.ld * sizeof(typename Elem<DT>::type);
+struct Chunk {
+    static constexpr int kN = Vec<DT>::kN;
+    int first, lane0, step;   // id of element e: first + lane0 + e * step
+    bool whole;
+    __device__ __forceinline__ Chunk(int first_, int n, int lane) : first(first_) {
+        whole = first + 64 * kN <= n;
+        lane0 = whole ? lane * kN : lane;
+        step = whole ? 1 : 64;
+    }
+    __device__ __forceinline__ int id(int e) const { return first + lane0 + e * step; }
+};
+// Its elements (-inf past the end), and bit e of `bits`: element e is allowed.
+template <int DT, bool MASKED>
+__device__ __forceinline__ void load_chunk(const Chunk<DT>& c,
+                                           const typename Elem<DT>::type* row,
+                                           const uint32_t* allow_row, int n, Vec<DT>& v,
+                                           uint32_t& bits) {
+    constexpr int N = Vec<DT>::kN;
+    bits = ~0u;
+    if (c.whole) {
+        __builtin_memcpy(v.w, row + c.id(0), 16);
+        if constexpr (MASKED) bits = allow_bits(allow_row, c.id(0), N);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.w[i] = kMinusInf<DT>;
+        if (c.first >= n) return;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int id = c.id(e);
+            if (id < n) {
+                const typename Elem<DT>::type one = row[id];
+                if constexpr (DT == FS_F32)
+                    v.w[e] = __builtin_bit_cast(uint32_t, one);
+                else
+                    v.w[e / 2] = (v.w[e / 2] & (e % 2 ? 0xFFFFu : 0xFFFF0000u)) |
+                                 ((uint32_t)__builtin_bit_cast(uint16_t, one) << (e % 2 * 16));
+                if constexpr (MASKED)
+                    if (!((allow_row[id >> 5] >> (id & 31)) & 1u)) bits &= ~(1u << e);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    return v;
+}
+
+// log2(e) / T, finite.
+__device__ __forceinline__ float exponent_scale(float T) {
+    return fminf(fminf(1.f / T, 3.402823466e38f) * kLog2e, 3.402823466e38f);
+}
+
+// One slice's state: m, S, A in units of ln 2, and how many ids come before
+// the token.
+struct Slice {
+    float m, S, A;
+    int before;
+};
+
+struct LogprobsWs {
+    Slice* part;      // [B][slices]
+    uint64_t* best;   // [B][slices][n_top] keys, best first, 0 past the last
+};
+
+__device__ __forceinline__ void write_row(const LogprobsArgs& a, int b, float T, float m, float S,
+                                          float A, int before, float lt, float logS) {
+    const bool any = m > -INFINITY, has = lt > -INFINITY;
+    if (a.logprob) a.logprob[b] = has ? (lt - m) / T - logS : -INFINITY;
+    if (a.rank) a.rank[b] = has ? before + 1 : 0;
+    if (a.lse) a.lse[b] = any ? m / T + logS : -INFINITY;
+    if (a.entropy) a.entropy[b] = any ? logS - kLn2 * (A / S) : 0.f;
+}
+__device__ __forceinline__ void write_best(const LogprobsArgs& a, int b, int j, uint64_t key,
+                                           float T, float m, float logS) {
+    const size_t o = (size_t)b * a.n_top + j;
+    a.top_idx[o] = key ? key_index(key) + a.v_offset : -1;
+    a.top_logprob[o] = key ? (key_score(key) - m) / T - logS : -INFINITY;
+}
+
+// The row's token as a local id, and its logit (-inf: none to look at).
+template <int DT>
+__device__ __forceinline__ float token_logit(const LogprobsArgs& a, const uint32_t* allow_row,
+                                             const typename Elem<DT>::type* row, int n, int b,
+                                             int& tok) {
+    tok = -1;
+    if (!a.token) return -INFINITY;
+    const int64_t t = (int64_t)a.token[b] - a.v_offset;
+    if (a.token[b] < 0 || t < 0 || t >= n) return -INFINITY;
+    tok = (int)t;
+    return allowed(allow_row, tok) ? clean((float)row[tok]) : -INFINITY;
+}
+
+// The largest float below x (x finite).
+__device__ __forceinline__ float below(float x) {
+    return x == 0.f ? __uint_as_float(0x80000001u) : ordered_to_float(float_to_ordered(x) - 1);
+}
+
+// The n-th largest of 256 keys k[4] (one wave, four a lane), or a smaller
+// value that at least n keys reach; sure == n: exactly n keys reach it.
+__device__ __forceinline__ uint32_t nth_largest(const uint32_t (&k)[4], int n, int& reach) {
+    uint32_t prefix = 0;
+    reach = kLpThreads;
+    for (int bit = 31; bit >= 0 && reach != n; --bit) {
+        const uint32_t cand = prefix | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c += __popcll(__ballot(k[i] >= cand));
+        if (c >= n) {
+            prefix = cand;
+            reach = c;
+        }
+    }
+    return prefix;
+}
+
+// Best alternatives of a slice held in registers.  The n-th largest of the
+// threads' maxima bounds the n-th largest element from below, and only
+// threads that reach it hold elements that do: about n elements are
+// collected, ranked by counting and written best first.  Where equal values
+// make the collection overflow, only the threads of the lowest ids among the
+// tied ones count: n threads, n E elements at most.
+template <int DT, int E>
+struct TopShared {
+    float tmax[kLpThreads];
+    int first[kLpThreads];
+    uint64_t key[kCandidates];
+    int count;
+    float bound;
+    int id_limit;
+};
+
+template <int DT, int E, typename F, typename I>
+__device__ void best_of_slice(TopShared<DT, E>& s, const float (&x)[E], float tmax, I id_of, int n,
+                              F write) {
+    const int t = threadIdx.x, lane = t & 63;
+    s.tmax[t] = tmax + 0.f;
+    if (t == 0) {
+        s.count = 0;
+        s.id_limit = 0x7FFFFFFF;
+    }
+    __syncthreads();
+    uint32_t bound = 0;
+    int reach = 0;
+    uint32_t k[4];
+    if (t < 64) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = float_to_ordered(s.tmax[lane + 64 * i]);
+        // (unmasked values only)
+        bound = max(nth_largest(k, n, reach), float_to_ordered(-INFINITY) + 1);
+        if (t == 0) s.bound = ordered_to_float(bound);
+    }
+    __syncthreads();
+    auto collect = [&]() {
+        const float lo = s.bound;
+        const int limit = s.id_limit;
+        if (tmax >= lo) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int id = id_of(e);
+                if (x[e] > lo || (x[e] == lo && id <= limit)) {
+                    const int at = atomicAdd(&s.count, 1);
+                    if (at < kCandidates) s.key[at] = pack_key(x[e] + 0.f, id);
+                }
+            }
+        }
+        __syncthreads();
+    };
+    collect();
+    if (s.count > kCandidates) {   // (the same for all threads)
+        int first = 0x7FFFFFFF;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (x[e] == s.bound) first = min(first, id_of(e));
+        s.first[t] = first;
+        __syncthreads();
+        if (t < 64) {
+            int above = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) above += __popcll(__ballot(k[i] > bound));
+            // the (n - above)-th lowest first id among the tied threads
+            uint32_t prefix = 0;
+            for (int bit = 30; bit >= 0; --bit) {
+                const uint32_t cand = prefix | ((1u << bit) - 1);
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    c += __popcll(__ballot((uint32_t)s.first[lane + 64 * i] <= cand));
+                if (c < n - above) prefix |= 1u << bit;
+            }
+            if (t == 0) {
+                s.id_limit = (int)prefix;
+                s.count = 0;
+            }
+        }
+        __syncthreads();
+        collect();
+    }
+    const int c = min(s.count, kCandidates);
+    for (int i = t; i < c; i += kLpThreads) {
+        const uint64_t mine = s.key[i];
+        int r = 0;
+        for (int j = 0; j < c; ++j) r += s.key[j] > mine;
+        if (r < n) write(r, mine);
+    }
+    for (int i = c + t; i < n; i += kLpThreads) write(i, (uint64_t)0);
+}
+
+// One slice of kLpThreads E elements of a row.
+template <int DT, int E, bool MASKED, bool TOP>
+__global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, LogprobsWs ws,
+                                                              int slices) {
+    typedef typename Elem<DT>::type T_;
+    constexpr int N = Vec<DT>::kN;
+    __shared__ float smax[kLpWaves], sS[kLpWaves], sA[kLpWaves];
+    __shared__ int sbefore[kLpWaves];
+    __shared__ std::conditional_t<TOP, TopShared<DT, E>, char> top;
+    const int n = valid_ids(a.V, a.n_valid, a.v_offset);
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int base = blockIdx.x * (kLpThreads * E);
+    for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+        // (formed per row: hoisted, the ids and their tests against n would
+        // take over a hundred registers)
+        int lane_id = lane;
+        asm volatile("" : "+v"(lane_id));
+        auto chunk = [&](int j) {
+            return Chunk<DT>(base + (j * kLpWaves + wave) * 64 * N, n, lane_id);
+        };
+        const T_* row = static_cast<const T_*>(a.logits) + (size_t)b * a.ld;
         const uint32_t* allow_row = a.allow ? a.allow + (size_t)b * ((a.V + 31) >> 5) : nullptr;
+        Vec<DT> raw[E / N];
+        uint32_t bits[E / N];
+#pragma unroll
+        for (int j = 0; j < E / N; ++j)
+            load_chunk<DT, MASKED>(chunk(j), row, allow_row, n, raw[j], bits[j]);
         const float T = row_temp(a.temp, b, a.flags);
-        float m = -INFINITY;
-        for (int i = threadIdx.x; i < Vv; i += kLpThreads)
-            m = fmaxf(m, row_logit<DT>(row, allow_row, i));
-        m = block_reduce(m, fslot, [](float x, float y) { return fmaxf(x, y); });
-        const int tok = a.token ? a.token[b] - a.v_offset : -1;
-        const float lt = tok >= 0 && tok < Vv ? row_logit<DT>(row, allow_row, tok) : -INFINITY;
+        int tok;
+        const float lt = token_logit<DT>(a, allow_row, row, n, b, tok);
+        float x[E];
+        float tmax = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[e] = clean(raw[e / N].at(e % N));
+            if constexpr (MASKED) x[e] = (bits[e / N] >> (e % N)) & 1u ? x[e] : -INFINITY;
+            tmax = fmaxf(tmax, x[e]);
+        }
+        const float wmax = wave_max(tmax);
+        if (lane == 0) smax[wave] = wmax;
+        __syncthreads();
+        const float m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+
+        const float c = exponent_scale(T);
+        const float from = m > -INFINITY ? m : 0.f;
+        const bool has = lt > -INFINITY;
+        const float lt_below = has ? below(lt) : INFINITY, lt_over = has ? lt : INFINITY;
         float S = 0.f, A = 0.f;
         int before = 0;
-        for (int i = threadIdx.x; i < Vv; i += kLpThreads) {
-            const float l = row_logit<DT>(row, allow_row, i);
-            if (!(l > -INFINITY)) continue;
-            const float x = (l - m) / T;
-            const float e = __expf(x);
-            S += e;
-            A += e > 0.f ? x * e : 0.f;
-            before += l > lt || (l == lt && i < tok);
+#pragma unroll
+        for (int j = 0; j < E / N; ++j) {
+            float S1 = 0.f, A1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float d = fmaxf((x[j * N + e] - from) * c, kFloor);
+                const float p = __builtin_amdgcn_exp2f(d);
+                S1 += p;
+                A1 = fmaf(d, p, A1);
+            }
+            S += S1;
+            A += A1;
+            // ids before the token: wholly before it, those that reach its
+            // logit; wholly behind it, those above
+            const Chunk<DT> ch = chunk(j);
+            if (ch.whole && (tok < ch.first || tok >= ch.first + 64 * N)) {
+                const float over = tok < ch.first ? lt_over : lt_below;
+#pragma unroll
+                for (int e = 0; e < N; ++e) before += x[j * N + e] > over ? 1 : 0;
+            } else if (has) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float v = x[j * N + e];
+                    before += v > lt || (v == lt && ch.id(e) < tok) ? 1 : 0;
+                }
+            }
         }
-        S = block_reduce(S, fslot, add);
-        A = block_reduce(A, fslot, add);
-        before = block_reduce(before, islot, [](int x, int y) { return x + y; });
-        const bool any = m > -INFINITY;
+        S = wave_sum(S);
+        A = wave_sum(A);
+        before = wave_sum(before);
+        if (lane == 0) {
+            sS[wave] = S;
+            sA[wave] = A;
+            sbefore[wave] = before;
+        }
+        __syncthreads();
+        S = (sS[0] + sS[1]) + (sS[2] + sS[3]);
+        A = (sA[0] + sA[1]) + (sA[2] + sA[3]);
+        before = sbefore[0] + sbefore[1] + sbefore[2] + sbefore[3];
         const float logS = logf(S);
-        if (threadIdx.x == 0) {
-            const bool has = lt > -INFINITY;
-            if (a.logprob) a.logprob[b] = has ? (lt - m) / T - logS : -INFINITY;
-            if (a.rank) a.rank[b] = has ? before + 1 : 0;
-            if (a.lse) a.lse[b] = any ? m / T + logS : -INFINITY;
-            if (a.entropy) a.entropy[b] = any ? logS - A / S : 0.f;
+        if (t == 0) {
+            if (slices == 1)
+                write_row(a, b, T, m, S, A, before, lt, logS);
+            else
+                ws.part[(size_t)b * slices + blockIdx.x] = Slice{m, S, A, before};
         }
-        uint64_t last = ~0ull;
-        for (int j = 0; j < a.n_top; ++j) {
-            uint64_t best = 0;
-            for (int i = threadIdx.x; i < Vv; i += kLpThreads) {
-                const float l = row_logit<DT>(row, allow_row, i);
-                const uint64_t k = l > -INFINITY ? pack_key(l, i) : 0;
-                if (k < last) best = key_max(best, k);
-            }
-            best = block_reduce(best, kslot, [](uint64_t x, uint64_t y) { return key_max(x, y); });
-            last = best;
-            if (threadIdx.x == 0) {
-                const size_t o = (size_t)b * a.n_top + j;
-                a.top_idx[o] = best ? key_index(best) + a.v_offset : -1;
-                a.top_logprob[o] = best ? (key_score(best) - m) / T - logS : -INFINITY;
-            }
+        if constexpr (TOP) {
+            uint64_t* out = ws.best + ((size_t)b * slices + blockIdx.x) * a.n_top;
+            auto id_of = [&](int e) { return chunk(e / N).id(e % N); };
+            best_of_slice<DT, E>(top, x, tmax, id_of, a.n_top, [&](int j, uint64_t key) {
+                if (slices == 1)
+                    write_best(a, b, j, key, T, m, logS);
+                else
+                    out[j] = key;
+            });
         }
+        __syncthreads();   // before the next row's shared values
     }
 }
 
-// dl_i = 1/T [ p_i (g_lse - g_lp - sum_j g_top_j - g_H (ln p_i + H))
-//              + [i = token] g_lp + sum_j [i = top_j] g_top_j ],  ln p_i = x_i - lse.
-template <int DT>
-__global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobsGradArgs a) {
-    typedef typename Elem<DT>::type E;
-    const int Vv = min((int64_t)a.V, max((int64_t)0, (int64_t)a.n_valid - a.v_offset));
-    for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-        const E* row = static_cast<const E*>(a.logits) + (size_t)b * a.ld;
-        E* out = static_cast<E*>(a.grad) + (size_t)b * a.ld_grad;
-        const uint32_t* allow_row = a.allow ? a.allow + (size_t)b * ((a.V + 31) >> 5) : nullptr;
+// Joins the slices of a row.  Alternatives: with at least n slices the n-th
+// best of their first entries bounds the row's n-th best from below, and at
+// most n lists reach it.
+__global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs a, LogprobsWs ws,
+                                                                   int slices) {
+    extern __shared__ __align__(16) uint64_t keys[];   // n_top * min(n_top, slices), heads
+    __shared__ float smax[kLpWaves], sS[kLpWaves], sA[kLpWaves];
+    __shared__ int sbefore[kLpWaves];
+    __shared__ int count;
+    __shared__ unsigned long long bound;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const Slice* part = ws.part + (size_t)b * slices;
         const float T = row_temp(a.temp, b, a.flags);
-        const float lse = a.lse[b];
-        const float glp = a.g_logprob ? a.g_logprob[b] : 0.f;
+        const float c = exponent_scale(T);
+        float m = -INFINITY;
+        for (int i = t; i < slices; i += kLpThreads) m = fmaxf(m, part[i].m);
+        m = wave_max(m);
+        if (lane == 0) smax[wave] = m;
+        if (t == 0) {
+            count = 0;
+            bound = 1;
+        }
+        __syncthreads();
+        m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+        const float from = m > -INFINITY ? m : 0.f;
+        float S = 0.f, A = 0.f;
+        int before = 0;
+        for (int i = t; i < slices; i += kLpThreads) {
+            const Slice p = part[i];
+            const float d = fmaxf((p.m - from) * c, kFloor);
+            const float w = __builtin_amdgcn_exp2f(d);
+            S = fmaf(p.S, w, S);
+            A = fmaf(w, fmaf(d, p.S, p.A), A);
+            before += p.before;
+        }
+        S = wave_sum(S);
+        A = wave_sum(A);
+        before = wave_sum(before);
+        if (lane == 0) {
+            sS[wave] = S;
+            sA[wave] = A;
+            sbefore[wave] = before;
+        }
+        __syncthreads();
+        S = (sS[0] + sS[1]) + (sS[2] + sS[3]);
+        A = (sA[0] + sA[1]) + (sA[2] + sA[3]);
+        before = sbefore[0] + sbefore[1] + sbefore[2] + sbefore[3];
+        const float logS = logf(S);
+        if (t == 0) {
+            // the token's logit once more (-inf: none to look at)
+            const int n = valid_ids(a.V, a.n_valid, a.v_offset);
+            const uint32_t* allow_row = a.allow ? a.allow + (size_t)b * ((a.V + 31) >> 5) : nullptr;
+            int tok;
+            float lt;
+            if (a.dtype == FS_F32)
+                lt = token_logit<FS_F32>(a, allow_row, static_cast<const float*>(a.logits) + (size_t)b * a.ld, n, b, tok);
+            else if (a.dtype == FS_BF16)
+                lt = token_logit<FS_BF16>(a, allow_row, static_cast<const __bf16*>(a.logits) + (size_t)b * a.ld, n, b, tok);
+            else
+                lt = token_logit<FS_F16>(a, allow_row, static_cast<const _Float16*>(a.logits) + (size_t)b * a.ld, n, b, tok);
+            write_row(a, b, T, m, S, A, before, lt, logS);
+        }
+        const int n = a.n_top;
+        if (n > 0) {
+            const uint64_t* best = ws.best + (size_t)b * slices * n;
+            if (slices > n) {
+                uint64_t* heads = keys + n * n;
+                const bool staged = slices <= kHeads;
+                if (staged)
+                    for (int i = t; i < slices; i += kLpThreads) heads[i] = best[(size_t)i * n];
+                __syncthreads();
+                for (int i = t; i < slices; i += kLpThreads) {
+                    const uint64_t mine = best[(size_t)i * n];
+                    int r = 0;
+                    for (int j = 0; j < slices; ++j)
+                        r += (staged ? heads[j] : best[(size_t)j * n]) > mine;
+                    if (r == n - 1 && mine) bound = mine;   // (keys differ: one thread)
+                }
+            }
+            __syncthreads();
+            const uint64_t lo = bound;
+            for (int64_t i = t; i < (int64_t)slices * n; i += kLpThreads) {
+                const uint64_t k = best[i];
+                if (k >= lo) keys[atomicAdd(&count, 1)] = k;
+            }
+            __syncthreads();
+            for (int i = t; i < count; i += kLpThreads) {
+                const uint64_t mine = keys[i];
+                int r = 0;
+                for (int j = 0; j < count; ++j) r += keys[j] > mine;
+                if (r < n) write_best(a, b, r, mine, T, m, logS);
+            }
+            for (int i = count + t; i < n; i += kLpThreads) write_best(a, b, i, 0, T, m, logS);
+        }
+        __syncthreads();
+    }
+}
+
+// Gradient: dl_i = 1/T [ p_i (c - g_H (ln p_i + H)) + [i = token] g_lp +
+// sum_j [i = top_j] g_top_j ],  c = g_lse - g_lp - sum_j g_top_j, ln p_i = x_i
+// - lse.  Bound by one read and one write of [B, V].
+constexpr int kGradElems = 16;   // per thread
+constexpr int kSpecials = kMaxAlternatives + 1;
+
+template <int DT, bool MASKED>
+__global__ __launch_bounds__(kLpThreads) void logprobs_grad_kernel(LogprobsGradArgs a) {
+    typedef typename Elem<DT>::type T_;
+    constexpr int N = Vec<DT>::kN;
+    constexpr int kSlice = kLpThreads * kGradElems;
+    __shared__ int special[kSpecials];
+    __shared__ float add[kSpecials];
+    __shared__ int nspecial;
+    __shared__ float sum_top;
+    const int n = valid_ids(a.V, a.n_valid, a.v_offset);
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int base = blockIdx.x * kSlice;
+    for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+        int lane_id = lane;   // (formed per row, as above)
+        asm volatile("" : "+v"(lane_id));
+        // chunks of the whole row of V: masked ids are written too
+        auto chunk = [&](int j) {
+            return Chunk<DT>(base + (j * kLpWaves + wave) * 64 * N, a.V, lane_id);
+        };
+        const T_* row = static_cast<const T_*>(a.logits) + (size_t)b * a.ld;
+        T_* out = static_cast<T_*>(a.grad) + (size_t)b * a.ld_grad;
+        const uint32_t* allow_row = a.allow ? a.allow + (size_t)b * ((a.V + 31) >> 5) : nullptr;
+        Vec<DT> raw[kGradElems / N];
+        uint32_t bits[kGradElems / N];
+#pragma unroll
+        for (int j = 0; j < kGradElems / N; ++j)
+            load_chunk<DT, MASKED>(chunk(j), row, allow_row, a.V, raw[j], bits[j]);
+        const float T = row_temp(a.temp, b, a.flags), inv_t = 1.f / T;
+        float lse = a.lse[b];
+        const bool ok = fabsf(lse) < INFINITY;
+        lse = ok ? lse : INFINITY;   // p = 0 everywhere
+        const int tok = a.g_logprob ? a.token[b] : -1;
+        const float glp = tok >= 0 ? a.g_logprob[b] : 0.f;
         const float gH = a.g_entropy ? a.g_entropy[b] : 0.f;
         const float H = a.g_entropy ? a.entropy[b] : 0.f;
-        const int tok_id = a.g_logprob ? a.token[b] : -1;
-        const int tok = tok_id >= 0 ? tok_id - a.v_offset : -1;
-        float c = (a.g_lse ? a.g_lse[b] : 0.f) - (tok_id >= 0 ? glp : 0.f);
-        for (int j = 0; a.g_top && j < a.n_top; ++j)
-            if (a.top_idx[(size_t)b * a.n_top + j] >= 0) c -= a.g_top[(size_t)b * a.n_top + j];
-        for (int i = blockIdx.x * kLpThreads + threadIdx.x; i < a.V; i += gridDim.x * kLpThreads) {
-            const float l = i < Vv ? row_logit<DT>(row, allow_row, i) : -INFINITY;
+        // the ids of this slice that get something added, by the first wave
+        if (t < 64) {
             float g = 0.f;
-            if (l > -INFINITY && fabsf(lse) < INFINITY) {
-                const float lp = l / T - lse;
-                const float p = __expf(lp);
-                g = p > 0.f ? p * (c - gH * (lp + H)) : 0.f;
-                if (i == tok) g += glp;
-                for (int j = 0; a.g_top && j < a.n_top; ++j)
-                    if (a.top_idx[(size_t)b * a.n_top + j] - a.v_offset == i)
-                        g += a.g_top[(size_t)b * a.n_top + j];
-                g /= T;
+            int id = -1;
+            if (a.g_top && t < a.n_top) {
+                id = a.top_idx[(size_t)b * a.n_top + t];
+                g = id >= 0 ? a.g_top[(size_t)b * a.n_top + t] : 0.f;
             }
-            out[i] = (E)g;
+            const float s = wave_sum(g);
+            const int64_t at = (int64_t)id - a.v_offset - base;
+            const bool here = ok && id >= 0 && at >= 0 && at < kSlice;
+            const uint64_t who = __ballot(here);
+            if (here) {
+                const int slot = __popcll(who & ((1ull << t) - 1));
+                special[slot] = (int)at;
+                add[slot] = g * inv_t;
+            }
+            if (t == 0) {
+                int k = __popcll(who);
+                const int64_t tat = (int64_t)tok - a.v_offset - base;
+                if (ok && tok >= 0 && tat >= 0 && tat < kSlice) {
+                    special[k] = (int)tat;
+                    add[k++] = glp * inv_t;
+                }
+                nspecial = k;
+                sum_top = s;
+            }
         }
+        __syncthreads();
+        const float gHt = gH * inv_t;
+        const float c = ((a.g_lse ? a.g_lse[b] : 0.f) - glp - sum_top) * inv_t - gHt * H;
+        const int ns = nspecial;
+#pragma unroll
+        for (int j = 0; j < kGradElems / N; ++j) {
+            const Chunk<DT> ch = chunk(j);
+            float g[N];
+            bool on[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float l = clean(raw[j].at(e));
+                on[e] = l > -INFINITY && ch.id(e) < n;
+                if constexpr (MASKED) on[e] = on[e] && ((bits[j] >> e) & 1u);
+                // l / T to FP32 accuracy, and not below what e^x makes 0
+                const float x0 = l * inv_t;
+                const float x = fmaf(fmaf(-x0, T, l), inv_t, x0);
+                const float lp = fmaxf(x - lse, -1e6f);
+                g[e] = on[e] ? __builtin_amdgcn_exp2f(lp * kLog2e) * (c - gHt * lp) : 0.f;
+            }
+            for (int k = 0; k < ns; ++k) {
+                const int at = base + special[k];
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (ch.id(e) == at && on[e]) g[e] += add[k];
+            }
+            if (ch.whole) {
+                T_ v[N];
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[e] = (T_)g[e];
+                __builtin_memcpy(out + ch.id(0), v, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (ch.id(e) < a.V) out[ch.id(e)] = (T_)g[e];
+            }
+        }
+        __syncthreads();   // before the next row's special ids
     }
 }
 
-hipError_t launch_logprobs(const LogprobsArgs& a, void* ws, hipStream_t stream) {
-    (void)ws;
-    const dim3 grid(a.B);
-    if (a.dtype == FS_F32)
-        hipLaunchKernelGGL(logprobs_kernel<FS_F32>, grid, dim3(kLpThreads), 0, stream, a);
-    else if (a.dtype == FS_BF16)
-        hipLaunchKernelGGL(logprobs_kernel<FS_BF16>, grid, dim3(kLpThreads), 0, stream, a);
+int slice_elems(int B, int V, int cus) {
+    // one slice where a workgroup holds the whole row (no second kernel);
+    // long slices once they fill the chip
+    const int64_t one = (int64_t)kLpThreads * kLpLong;
+    if (V <= kLpThreads * kLpShort) return kLpThreads * kLpShort;
+    if (V <= one || (int64_t)B * ((V + one - 1) / one) >= 2 * cus) return (int)one;
+    return kLpThreads * kLpShort;
+}
+
+LogprobsWs carve(const LogprobsArgs& a, void* ws, int slices) {
+    LogprobsWs w;
+    w.part = static_cast<Slice*>(ws);
+    w.best = reinterpret_cast<uint64_t*>(w.part + (size_t)a.B * slices);
+    return w;
+}
+
+template <int DT, int E, bool MASKED>
+void launch_slices(const LogprobsArgs& a, const LogprobsWs& w, int slices, hipStream_t stream) {
+    const dim3 grid(slices, a.B < kMaxGridY ? a.B : kMaxGridY);
+    if (a.n_top > 0)
+        hipLaunchKernelGGL((logprobs_kernel<DT, E, MASKED, true>), grid, dim3(kLpThreads), 0,
+                           stream, a, w, slices);
     else
-        hipLaunchKernelGGL(logprobs_kernel<FS_F16>, grid, dim3(kLpThreads), 0, stream, a);
+        hipLaunchKernelGGL((logprobs_kernel<DT, E, MASKED, false>), grid, dim3(kLpThreads), 0,
+                           stream, a, w, slices);
+}
+
+template <int DT>
+void launch_type(const LogprobsArgs& a, const LogprobsWs& w, int slices, bool lng,
+                 hipStream_t stream) {
+    if (lng)
+        a.allow ? launch_slices<DT, kLpLong, true>(a, w, slices, stream)
+                : launch_slices<DT, kLpLong, false>(a, w, slices, stream);
+    else
+        a.allow ? launch_slices<DT, kLpShort, true>(a, w, slices, stream)
+                : launch_slices<DT, kLpShort, false>(a, w, slices, stream);
+}
+
+}  // namespace
+
+size_t logprobs_ws_bytes(int B, int V, int n_top, int cus) {
+    const int per = slice_elems(B, V, cus);
+    const size_t slices = V > 0 ? ((size_t)V + per - 1) / per : 1;
+    return slices > 1 ? (size_t)B * slices * (sizeof(Slice) + 8 * (size_t)n_top) : 0;
+}
+
+hipError_t launch_logprobs(const LogprobsArgs& a, void* ws, int cus, hipStream_t stream) {
+    const int per = slice_elems(a.B, a.V, cus);
+    const int slices = a.V > 0 ? (int)(((int64_t)a.V + per - 1) / per) : 1;
+    const LogprobsWs w = carve(a, ws, slices);
+    const bool lng = per == kLpThreads * kLpLong;
+    if (a.dtype == FS_F32)
+        launch_type<FS_F32>(a, w, slices, lng, stream);
+    else if (a.dtype == FS_BF16)
+        launch_type<FS_BF16>(a, w, slices, lng, stream);
+    else
+        launch_type<FS_F16>(a, w, slices, lng, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || slices == 1) return e;
+    // at most 40 KiB
+    const size_t lds = 8 * ((size_t)a.n_top * std::min(a.n_top, slices) + std::min(slices, kHeads));
+    hipLaunchKernelGGL(logprobs_join_kernel, dim3(a.B), dim3(kLpThreads), lds, stream, a, w, slices);
     return hipGetLastError();
 }
 
 hipError_t launch_logprobs_grad(const LogprobsGradArgs& a, hipStream_t stream) {
-    const dim3 grid((a.V + 4095) / 4096, a.B < kMaxGridY ? a.B : kMaxGridY);
-    if (a.dtype == FS_F32)
-        hipLaunchKernelGGL(logprobs_grad_kernel<FS_F32>, grid, dim3(kLpThreads), 0, stream, a);
-    else if (a.dtype == FS_BF16)
-        hipLaunchKernelGGL(logprobs_grad_kernel<FS_BF16>, grid, dim3(kLpThreads), 0, stream, a);
-    else
-        hipLaunchKernelGGL(logprobs_grad_kernel<FS_F16>, grid, dim3(kLpThreads), 0, stream, a);
+    const dim3 grid((unsigned)(((int64_t)a.V + kLpThreads * kGradElems - 1) / (kLpThreads * kGradElems)),
+                    a.B < kMaxGridY ? a.B : kMaxGridY);
+#define FS_LG(DT_, M_)                                                                          \
+    if (a.dtype == DT_ && (a.allow != nullptr) == M_)                                           \
+        hipLaunchKernelGGL((logprobs_grad_kernel<DT_, M_>), grid, dim3(kLpThreads), 0, stream, a);
+    FS_LG(FS_F32, false)
+    FS_LG(FS_F32, true)
+    FS_LG(FS_BF16, false)
+    FS_LG(FS_BF16, true)
+    FS_LG(FS_F16, false)
+    FS_LG(FS_F16, true)
+#undef FS_LG
     return hipGetLastError();
 }
 

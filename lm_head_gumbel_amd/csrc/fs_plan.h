@@ -162,6 +162,9 @@ fs_status check_params(const fs_params* p);
 // The same for the operators that take any hidden size (or read none).
 fs_status check_params_any_d(const fs_params* p);
 constexpr int kMaxAlternatives = 64;   // n_top of fs_logprobs
+// Ids of a row of fs_logprobs and its gradient: ids past the last, up to the
+// end of the last slice, still fit an int.
+constexpr int kMaxRow = INT32_MAX - 65536;
 // Plan of a call that passed check_params with B > 0 and V > 0, on a device
 // with `cus` compute units.  variant: Stage1Variant.
 void make_plan(const fs_params* p, int variant, int cus, Plan& pl);

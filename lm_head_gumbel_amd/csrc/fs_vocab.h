@@ -53,7 +53,9 @@ struct LogprobsArgs {
     int32_t* top_idx;
     float* top_logprob;
 };
-hipError_t launch_logprobs(const LogprobsArgs& a, void* ws, hipStream_t stream);
+// Workspace of a call (0: none), the same cus as the launch.
+size_t logprobs_ws_bytes(int B, int V, int n_top, int cus);
+hipError_t launch_logprobs(const LogprobsArgs& a, void* ws, int cus, hipStream_t stream);
 
 struct LogprobsGradArgs {
     const void* logits;
@@ -98,13 +100,6 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, void* ws, hipStream_t strea
 __device__ __forceinline__ float row_temp(const float* temp, int b, uint32_t flags) {
     const float T = temp ? temp[b] : 1.f;
     return (flags & kFlagNoNoise) || !(T > 0.f) ? 1.f : T;
-}
-
-// FP32 logit of an unmasked id as the operators see it: NaN counts as masked,
-// +inf as the largest finite value, -0 as 0.
-__device__ __forceinline__ float clean_logit(float l) {
-    l = l == l ? l : -INFINITY;
-    return fminf(l, 3.402823466e38f) + 0.f;
 }
 
 __device__ __forceinline__ bool allowed(const uint32_t* allow_row, int i) {
