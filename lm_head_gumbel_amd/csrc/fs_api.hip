@@ -217,7 +217,8 @@ size_t fs_workspace_bytes(const fs_params* p, int variant, int32_t k) {
     if (variant == FS_VARIANT_LOGPROBS || variant == FS_VARIANT_EMBED_GRAD) {
         DeviceInfo dev;
         if (check_params_any_d(p) != FS_OK || !current_device(dev)) return 0;
-        if (variant == FS_VARIANT_EMBED_GRAD) return kAlign;
+        if (variant == FS_VARIANT_EMBED_GRAD)
+            return std::max(kAlign, embed_grad_ws_bytes(p->B, p->d));
         if (k < 0 || k > kMaxAlternatives || p->V > kMaxRow) return 0;
         return std::max(kAlign, logprobs_ws_bytes(p->B, p->V, k, dev.cus));
     }
@@ -496,7 +497,7 @@ fs_status fs_logprobs(const fs_params* p, const void* logits, int dtype, int64_t
     if (!current_device(dev)) return FS_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < std::max(kAlign, logprobs_ws_bytes(p->B, p->V, n_top, dev.cus)))
         return FS_ERR_WORKSPACE;
-    if (reinterpret_cast<uintptr_t>(ws) % 16 != 0) return FS_ERR_UNSUPPORTED;
+    if (!aligned16(ws)) return FS_ERR_UNSUPPORTED;
     const LogprobsArgs a{logits, dtype, ld, temp, allow, token, p->B, p->V, p->n_valid,
                          p->v_offset, n_top, p->flags, out_logprob, out_rank, out_lse,
                          out_entropy, top_idx, top_logprob};
@@ -554,8 +555,9 @@ fs_status fs_embed_grad(const fs_params* p, const int32_t* ids, const void* g, i
     if (!elem_aligned(g, dtype) || !elem_aligned(dW, dw_dtype)) return FS_ERR_UNSUPPORTED;
     DeviceInfo dev;
     if (!current_device(dev)) return FS_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < fs_workspace_bytes(p, FS_VARIANT_EMBED_GRAD, 0))
+    if (!ws || ws_bytes < std::max(kAlign, embed_grad_ws_bytes(p->B, p->d)))
         return FS_ERR_WORKSPACE;
+    if (!aligned16(ws)) return FS_ERR_UNSUPPORTED;
     const EmbedGradArgs a{ids, g, dW, p->B, p->d, p->V, p->v_offset, dtype, dw_dtype, scale,
                           accumulate};
     return from_hip(launch_embed_grad(a, ws, static_cast<hipStream_t>(stream)));

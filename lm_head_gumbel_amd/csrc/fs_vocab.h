@@ -94,6 +94,7 @@ struct EmbedGradArgs {
     float scale;
     int accumulate;
 };
+size_t embed_grad_ws_bytes(int N, int d);
 hipError_t launch_embed_grad(const EmbedGradArgs& a, void* ws, hipStream_t stream);
 
 // A row's temperature: 1 where it is greedy, as the shared definitions say.
