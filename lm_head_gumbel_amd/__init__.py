@@ -50,9 +50,10 @@ def quant(q, scale, zero, group, scale_dtype=None):
     """Build an fs_quant from q [V, d / 2] uint8, scale [V, d / group] and zero
     (uint8 [V, d / group] or None): tensors, which it keeps alive, or raw
     addresses (then scale_dtype must be given)."""
-    if not _ready(q, scale, zero):
+    at = _operands((q, scale, zero))
+    if at is None:
         raise ValueError("quant: tensors must be contiguous and on the current device")
-    w = fs_quant(_ptr(q), _ptr(scale), _ptr(zero), group, _dtype(scale, scale_dtype))
+    w = fs_quant(*at, group, _dtype(scale, scale_dtype))
     w.tensors = (q, scale, zero)
     return w
 
@@ -144,50 +145,71 @@ def _ptr(x):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        if not torch.cuda.is_available():
+        dev = _device()
+        if dev is None:
             return None          # no device: the call fails validation or reports it
-        return torch.cuda.current_stream().cuda_stream
+        return _torch._C._cuda_getCurrentRawStream(dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-def _ready(*xs):
-    """Whether every tensor among xs is contiguous and on the current device
-    (raw addresses and None pass)."""
-    dev = None
+_torch = None   # torch, once it has a device
+
+
+def _device():
+    """The current device's index, or None without one."""
+    global _torch
+    if _torch is None:
+        import torch
+        if not torch.cuda.is_available():
+            return None
+        torch.cuda.init()
+        _torch = torch
+    return _torch._C._cuda_getDevice()
+
+
+def _operands(xs):
+    """The addresses of xs (tensors, raw addresses or None); None if a tensor
+    is not contiguous or not on the current device."""
+    dev = _device()
+    out = []
     for x in xs:
-        if x is None or isinstance(x, int):
-            continue
-        if not x.is_cuda or not x.is_contiguous():
-            return False
-        if dev is None:
-            import torch
-            dev = torch.cuda.current_device()
-        if x.get_device() != dev:
-            return False
-    return True
+        if x is None or x.__class__ is int:
+            out.append(x)
+        elif x.get_device() != dev or not x.is_contiguous():
+            return None
+        else:
+            out.append(x.data_ptr())
+    return out
+
+
+_DTYPES = {}
 
 
 def _dtype(x, dtype):
     """The element type of tensor x, or `dtype` where that is given (-1: none)."""
-    if dtype is not None or x is None or isinstance(x, int):
+    if dtype is not None or x is None or x.__class__ is int:
         return -1 if dtype is None else dtype
-    return {"torch.float32": FS_F32, "torch.bfloat16": FS_BF16, "torch.float16": FS_F16}.get(
-        str(x.dtype), -1)
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: FS_F32, torch.bfloat16: FS_BF16, torch.float16: FS_F16})
+    return _DTYPES.get(x.dtype, -1)
 
 
 def _rows(x, p, ld):
-    """Row distance in elements of a [B, V] operand whose rows are contiguous
-    (-1: it has no such layout, or is not of p's shape)."""
-    if ld is not None or x is None or isinstance(x, int):
-        return p.V if ld is None else ld
-    if x.dim() != 2 or x.shape[0] != p.B or x.shape[1] != p.V or (p.V > 1 and x.stride(1) != 1):
-        return -1
-    if not _ready(x[:0]):
-        return -1
-    return x.stride(0) if p.B > 1 else max(p.V, x.stride(0))
+    """Address and row distance in elements of a [B, V] operand whose rows are
+    contiguous (distance -1: it has no such layout, is not of p's shape or not
+    on the current device)."""
+    if x is None or x.__class__ is int:
+        return x, p.V if ld is None else ld
+    if x.dim() != 2 or x.get_device() != _device():
+        return None, -1
+    rows, cols = x.shape
+    step, one = x.stride()
+    if rows != p.B or cols != p.V or (cols > 1 and one != 1):
+        return None, -1
+    return x.data_ptr(), step if rows > 1 and ld is None else max(cols, step) if ld is None else ld
 
 
 def _ws(ws, ws_bytes):
@@ -292,54 +314,53 @@ def fs_multinomial(p, logits, temp, allow, out_idx, ws=None, ws_bytes=None, stre
 # device than the current one is FS_ERR_INVALID_ARG.
 
 def fs_logits_quant(p, H, W, logits, stream=None):
-    if not _ready(H, logits):
+    at = _operands((H, logits))
+    if at is None:
         return FS_ERR_INVALID_ARG
-    return lib().fs_logits_quant(ctypes.byref(p), _ptr(H), None if W is None else ctypes.byref(W),
-                                 _ptr(logits), _stream(stream))
+    return lib().fs_logits_quant(ctypes.byref(p), at[0], None if W is None else ctypes.byref(W),
+                                 at[1], _stream(stream))
 
 
 def fs_logprobs(p, logits, temp, allow, token, n_top, out_logprob=None, out_rank=None,
                 out_lse=None, out_entropy=None, top_idx=None, top_logprob=None, ws=None,
                 ws_bytes=None, stream=None, dtype=None, ld=None):
-    if not _ready(temp, allow, token, out_logprob, out_rank, out_lse, out_entropy, top_idx,
-                  top_logprob, ws):
+    at = _operands((temp, allow, token, out_logprob, out_rank, out_lse, out_entropy, top_idx,
+                    top_logprob, ws))
+    if at is None:
         return FS_ERR_INVALID_ARG
-    w, n = _ws(ws, ws_bytes)
-    return lib().fs_logprobs(ctypes.byref(p), _ptr(logits), _dtype(logits, dtype),
-                             _rows(logits, p, ld), _ptr(temp), _ptr(allow), _ptr(token), n_top,
-                             _ptr(out_logprob), _ptr(out_rank), _ptr(out_lse), _ptr(out_entropy),
-                             _ptr(top_idx), _ptr(top_logprob), w, n, _stream(stream))
+    rows, ld = _rows(logits, p, ld)
+    return lib().fs_logprobs(ctypes.byref(p), rows, _dtype(logits, dtype), ld, at[0], at[1], at[2],
+                             n_top, at[3], at[4], at[5], at[6], at[7], at[8], *_ws(ws, ws_bytes),
+                             _stream(stream))
 
 
 def fs_logprobs_grad(p, logits, temp, allow, token, n_top, top_idx, lse, entropy, g_logprob, g_lse,
                      g_entropy, g_top, grad, stream=None, dtype=None, ld=None, ld_grad=None):
-    if not _ready(temp, allow, token, top_idx, lse, entropy, g_logprob, g_lse, g_entropy, g_top):
-        return FS_ERR_INVALID_ARG
+    at = _operands((temp, allow, token, top_idx, lse, entropy, g_logprob, g_lse, g_entropy, g_top))
     dt = _dtype(logits, dtype)
-    if _dtype(grad, dtype) != dt:
+    if at is None or _dtype(grad, dtype) != dt:
         return FS_ERR_INVALID_ARG
-    return lib().fs_logprobs_grad(ctypes.byref(p), _ptr(logits), dt, _rows(logits, p, ld),
-                                  _ptr(temp), _ptr(allow), _ptr(token), n_top, _ptr(top_idx),
-                                  _ptr(lse), _ptr(entropy), _ptr(g_logprob), _ptr(g_lse),
-                                  _ptr(g_entropy), _ptr(g_top), _ptr(grad),
-                                  _rows(grad, p, ld_grad), _stream(stream))
+    rows, ld = _rows(logits, p, ld)
+    out, ld_grad = _rows(grad, p, ld_grad)
+    return lib().fs_logprobs_grad(ctypes.byref(p), rows, dt, ld, at[0], at[1], at[2], n_top,
+                                  *at[3:], out, ld_grad, _stream(stream))
 
 
 def fs_embed(p, ids, W, scale, out, stream=None, dtype=None):
+    at = _operands((ids, W, out))
     dt = _dtype(W, dtype)
-    if not _ready(ids, W, out) or _dtype(out, dtype) != dt:
+    if at is None or _dtype(out, dtype) != dt:
         return FS_ERR_INVALID_ARG
-    return lib().fs_embed(ctypes.byref(p), _ptr(ids), _ptr(W), dt, scale, _ptr(out),
-                          _stream(stream))
+    return lib().fs_embed(ctypes.byref(p), at[0], at[1], dt, scale, at[2], _stream(stream))
 
 
 def fs_embed_grad(p, ids, g, scale, accumulate, dW, ws=None, ws_bytes=None, stream=None,
                   dtype=None, dw_dtype=None):
-    if not _ready(ids, g, dW, ws):
+    at = _operands((ids, g, dW, ws))
+    if at is None:
         return FS_ERR_INVALID_ARG
-    w, n = _ws(ws, ws_bytes)
-    return lib().fs_embed_grad(ctypes.byref(p), _ptr(ids), _ptr(g), _dtype(g, dtype), scale,
-                               accumulate, _ptr(dW), _dtype(dW, dw_dtype), w, n, _stream(stream))
+    return lib().fs_embed_grad(ctypes.byref(p), at[0], at[1], _dtype(g, dtype), scale, accumulate,
+                               at[2], _dtype(dW, dw_dtype), *_ws(ws, ws_bytes), _stream(stream))
 
 
 def fs_debug_noise(seed, step, stream_id, b0, nb, i0, ni, words=None, gumbel=None, stream=None):

@@ -323,86 +323,96 @@ __device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t row, int k,
     store_row<DO, N>(out, k, a.d, x);
 }
 
-// Zeros in the rows row0 .. row0 + kZeroRows - 1 that no token names.
+// Zeros in the rows row0 .. row0 + kZeroRows - 1 that no token names: 256
+// probes of the sorted keys narrow the rows' tokens to a stretch, which is
+// read and marked.
 template <int DO>
-__device__ void zero_rows(const SumArgs& a, int row0) {
+__device__ void zero_rows(const SumArgs& a, uint32_t row0) {
     typedef typename Elem<DO>::type O;
     constexpr int N = 16 / (int)sizeof(O);
-    __shared__ uint64_t empty;
+    __shared__ uint32_t named[kZeroRows / 32];
     const int t = threadIdx.x;
-    if (t < 64) {
-        const uint32_t row = (uint32_t)row0 + t;
-        int lo = 0, hi = a.N;   // the first token with key >= row
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (a.key[mid] < row)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        const bool none = row < (uint32_t)a.V && !(lo < a.N && a.key[lo] == row);
-        const uint64_t m = __ballot(none);
-        if (t == 0) empty = m;
+    if (t < kZeroRows / 32) named[t] = 0;
+    const int step = max(1, (a.N + kEmThreads - 1) / kEmThreads);
+    const bool in = (int64_t)t * step < a.N;
+    const uint32_t probe = in ? a.key[t * step] : ~0u;
+    const int below = __syncthreads_count(in && probe < row0);
+    const int upto = __syncthreads_count(in && probe < row0 + kZeroRows);
+    const int i1 = (int)min((int64_t)upto * step, (int64_t)a.N);
+    for (int i = max(0, (below - 1) * step) + t; i < i1; i += kEmThreads) {
+        const uint32_t r = a.key[i] - row0;
+        if (r < kZeroRows) atomicOr(&named[r / 32], 1u << (r % 32));
     }
     __syncthreads();
-    uint64_t left = empty;
-    __syncthreads();   // before the next rows' flags
     const float zero[N] = {};
-    while (left) {
-        const int r = __ffsll((unsigned long long)left) - 1;
-        left &= left - 1;
-        O* out = static_cast<O*>(a.dW) + (size_t)(row0 + r) * a.d;
-        for (int k = t * N; k < a.d; k += kEmThreads * N) store_row<DO, N>(out, k, a.d, zero);
-    }
+    for (int w = 0; w < kZeroRows / 32; ++w)
+        for (uint32_t left = ~named[w]; left; left &= left - 1) {
+            const uint32_t row = row0 + w * 32 + __builtin_ctz(left);
+            if (row >= (uint32_t)a.V) break;
+            O* out = static_cast<O*>(a.dW) + (size_t)row * a.d;
+            for (int k = t * N; k < a.d; k += kEmThreads * N) store_row<DO, N>(out, k, a.d, zero);
+        }
+    __syncthreads();   // before the next rows' marks
+}
+// Workgroup i of the wgs behind a kernel's own that fill with zeros.
+template <int DO>
+__device__ void zero_part(const SumArgs& a, int i, int wgs) {
+    for (int64_t r = (int64_t)i * kZeroRows; r < a.V; r += (int64_t)wgs * kZeroRows)
+        zero_rows<DO>(a, (uint32_t)r);
 }
 
+// Sums of the chunks: `lanes` threads per chunk and column block.
 template <int DT, int DO>
 __global__ __launch_bounds__(kEmThreads) void embed_sum_kernel(SumArgs a) {
     typedef typename Elem<DT>::type E;
     constexpr int N = Row16<DT>::kN;
     if ((int)blockIdx.x >= a.sum_wgs) {
-        for (int64_t r = (int64_t)((int)blockIdx.x - a.sum_wgs) * kZeroRows; r < a.V;
-             r += (int64_t)((int)gridDim.x - a.sum_wgs) * kZeroRows)
-            zero_rows<DO>(a, (int)r);
+        zero_part<DO>(a, (int)blockIdx.x - a.sum_wgs, (int)gridDim.x - a.sum_wgs);
         return;
     }
     const int per = kEmThreads / a.lanes;   // chunks per workgroup
     const int sub = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes;
-    const int64_t c = (int64_t)(blockIdx.x / a.col_blocks) * per + sub;
+    const int64_t c0 = (int64_t)(blockIdx.x / a.col_blocks) * per;
     const int k = ((int)(blockIdx.x % a.col_blocks) * a.lanes + lane) * N;
-    const int64_t i0 = c * kChunk;
-    if (i0 >= a.N || k >= a.d) return;
-    const int i1 = (int)min(i0 + kChunk, (int64_t)a.N);
+    // the chunks' rows and tokens, with the row before the first and the one
+    // behind the last (none: ~0)
+    extern __shared__ uint32_t list[];   // per kChunk + 2 rows, per kChunk tokens
+    uint32_t* toks = list + per * kChunk + 2;
+    const int64_t base = c0 * kChunk;
+    for (int i = threadIdx.x; i < per * kChunk + 2; i += kEmThreads) {
+        const int64_t at = base + i - 1;
+        list[i] = at >= 0 && at < a.N ? a.key[at] : ~0u;
+    }
+    for (int i = threadIdx.x; i < per * kChunk; i += kEmThreads)
+        toks[i] = base + i < a.N ? a.pos[base + i] : 0;
+    __syncthreads();
+    const int64_t c = c0 + sub;
+    if (c * kChunk >= a.N || k >= a.d) return;
+    const uint32_t* rows = list + sub * kChunk + 1;
+    const uint32_t* tok = toks + sub * kChunk;
+    const int len = (int)min((int64_t)kChunk, a.N - c * kChunk);
     const E* g = static_cast<const E*>(a.g);
     float acc[N] = {};
-    // the run at i0 began in an earlier chunk
-    bool head = i0 > 0 && a.key[i0 - 1] == a.key[i0];
-    constexpr int kAhead = 4;   // rows of g in flight
-    for (int i = (int)i0; i < i1; i += kAhead) {
+    bool head = rows[-1] == rows[0];   // the first run began in an earlier chunk
+    constexpr int kAhead = 8;          // rows of g in flight
+    for (int i = 0; i < len; i += kAhead) {
         float x[kAhead][N];
-        uint32_t row[kAhead + 1];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i + u < len && rows[i + u] < (uint32_t)a.V)
+                load_row<DT>(g + (size_t)tok[i + u] * a.d, k, a.d, x[u]);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int iu = min(i + u, a.N - 1);
-            row[u] = a.key[iu];
-            if (row[u] < (uint32_t)a.V && i + u < i1)
-                load_row<DT>(g + (size_t)a.pos[iu] * a.d, k, a.d, x[u]);
-        }
-        row[kAhead] = i + kAhead < a.N ? a.key[i + kAhead] : ~0u;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (i + u >= i1 || row[u] >= (uint32_t)a.V) break;   // (none: sorted last)
+            if (i + u >= len || rows[i + u] >= (uint32_t)a.V) break;   // (none: sorted last)
+            const uint32_t row = rows[i + u];
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[e] += x[u][e];
-            const bool more = i + u + 1 < a.N && row[u + 1] == row[u];   // the run goes on
-            const bool end = i + u + 1 == i1;
-            if (more && !end) continue;
-            if (head || more) {
-                float* p = a.part + ((size_t)c * 2 + (head ? 0 : 1)) * a.d;
-                store_row<FS_F32, N>(p, k, a.d, acc);
-            } else {
-                write_sum<DO, N>(a, row[u], k, acc);
-            }
+            const bool more = rows[i + u + 1] == row;   // the run goes on
+            if (more && i + u + 1 < len) continue;
+            if (head || more)
+                store_row<FS_F32, N>(a.part + ((size_t)c * 2 + (head ? 0 : 1)) * a.d, k, a.d, acc);
+            else
+                write_sum<DO, N>(a, row, k, acc);
             head = false;
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[e] = 0.f;
@@ -411,9 +421,14 @@ __global__ __launch_bounds__(kEmThreads) void embed_sum_kernel(SumArgs a) {
 }
 
 // Runs over several chunks: the chunk where a run begins adds up its parts.
+// (The zeros ride here, where they hide the long runs' latency.)
 template <int DT, int DO>
 __global__ __launch_bounds__(kEmThreads) void embed_join_kernel(SumArgs a, int chunks) {
     constexpr int N = Row16<DT>::kN;
+    if ((int)blockIdx.x >= a.sum_wgs) {
+        zero_part<DO>(a, (int)blockIdx.x - a.sum_wgs, (int)gridDim.x - a.sum_wgs);
+        return;
+    }
     const int per = kEmThreads / a.lanes;
     const int sub = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes;
     const int64_t c = (int64_t)(blockIdx.x / a.col_blocks) * per + sub;
@@ -421,17 +436,32 @@ __global__ __launch_bounds__(kEmThreads) void embed_join_kernel(SumArgs a, int c
     if (c + 1 >= chunks || k >= a.d) return;
     const int64_t next = (c + 1) * kChunk;   // the next chunk's first token
     const uint32_t row = a.key[next];
-    if (row >= (uint32_t)a.V || a.key[next - 1] != row) return;          // no run crosses
-    if (c > 0 && a.key[next - kChunk - 1] == row) return;                // it began earlier
+    if (row >= (uint32_t)a.V || a.key[next - 1] != row) return;   // no run crosses
+    if (c > 0 && a.key[next - kChunk - 1] == row) return;         // it began earlier
+    auto load_part = [&](int64_t chunk, int tail, float* x) {
+        const float* p = a.part + ((size_t)chunk * 2 + tail) * a.d;
+        load_row<FS_F32>(p, k, a.d, x);
+        if constexpr (N > 4) load_row<FS_F32>(p, k + 4, a.d, x + 4);
+    };
     float acc[N];
-    load_row<FS_F32>(a.part + ((size_t)c * 2 + 1) * a.d, k, a.d, acc);
-    if constexpr (N > 4) load_row<FS_F32>(a.part + ((size_t)c * 2 + 1) * a.d, k + 4, a.d, acc + 4);
-    for (int64_t j = c + 1; j < chunks && a.key[j * kChunk] == row; ++j) {
-        float x[N];
-        load_row<FS_F32>(a.part + (size_t)j * 2 * a.d, k, a.d, x);
-        if constexpr (N > 4) load_row<FS_F32>(a.part + (size_t)j * 2 * a.d, k + 4, a.d, x + 4);
+    load_part(c, 1, acc);
+    constexpr int kAhead = 8;
+    bool more = true;
+    for (int64_t j = c + 1; more; j += kAhead) {
+        float x[kAhead][N];
+        bool on[kAhead];
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] += x[e];
+        for (int u = 0; u < kAhead; ++u) {
+            on[u] = j + u < chunks && a.key[(j + u) * kChunk] == row;
+            if (on[u]) load_part(j + u, 0, x[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            more = more && on[u];
+            if (more)
+#pragma unroll
+                for (int e = 0; e < N; ++e) acc[e] += x[u][e];
+        }
     }
     write_sum<DO, N>(a, row, k, acc);
 }
@@ -472,19 +502,22 @@ template <int DT, int DO>
 hipError_t launch_sums(const EmbedGradArgs& a, SumArgs s, hipStream_t stream) {
     const int N = Row16<DT>::kN;
     const int vecs = (a.d + N - 1) / N;
-    s.lanes = lanes_for(vecs);
+    s.lanes = std::max(4, lanes_for(vecs));   // (at most 64 chunks' lists per workgroup)
     s.col_blocks = (vecs + s.lanes - 1) / s.lanes;
     const int chunks = (a.N + kChunk - 1) / kChunk;
     const int per = kEmThreads / s.lanes;
     s.sum_wgs = (chunks + per - 1) / per * s.col_blocks;
     const int zero_wgs =
         a.accumulate ? 0 : (int)std::min(((int64_t)a.V + kZeroRows - 1) / kZeroRows, kMaxGridX);
-    hipLaunchKernelGGL((embed_sum_kernel<DT, DO>), dim3(s.sum_wgs + zero_wgs), dim3(kEmThreads), 0,
-                       stream, s);
+    const size_t lds = 4 * (size_t)(2 * per * kChunk + 2);   // at most 16 KiB + 8
+    const int here = chunks < 2 ? zero_wgs : 0;
+    if (s.sum_wgs + here > 0)
+        hipLaunchKernelGGL((embed_sum_kernel<DT, DO>), dim3(s.sum_wgs + here), dim3(kEmThreads),
+                           lds, stream, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || chunks < 2) return e;
-    hipLaunchKernelGGL((embed_join_kernel<DT, DO>), dim3(s.sum_wgs), dim3(kEmThreads), 0, stream, s,
-                       chunks);
+    hipLaunchKernelGGL((embed_join_kernel<DT, DO>), dim3(s.sum_wgs + zero_wgs), dim3(kEmThreads), 0,
+                       stream, s, chunks);
     return hipGetLastError();
 }
 

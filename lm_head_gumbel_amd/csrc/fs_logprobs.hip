@@ -23,10 +23,10 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWaves = kLpThreads / 64;
 constexpr int kLpShort = 8;    // elements per thread of a short slice
 constexpr int kLpLong = 32;    // and of a long one
-constexpr int kHeads = 1024;   // slices whose first entries the join keeps in LDS
-constexpr int kCandidates = kMaxAlternatives * kLpLong;
+constexpr int kJoinEntries = 2048;   // alternatives of a row's slices that the join keeps in LDS
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kMaxFloat = 3.402823466e38f;
 constexpr float kFloor = -1e30f;   // exponents: e^{-inf} without inf * 0
 
 // 16 bytes of elements as they lie in memory, four 32-bit words.
@@ -54,7 +54,7 @@ __device__ __forceinline__ int valid_ids(int V, int n_valid, int v_offset) {
 
 // FP32 logit: NaN -> -inf, +inf -> the largest finite value.
 __device__ __forceinline__ float clean(float l) {
-    return fminf(l == l ? l : -INFINITY, 3.402823466e38f);
+    return fminf(l == l ? l : -INFINITY, kMaxFloat);
 }
 
 // Bit o of the result: id i + o is allowed (o < n <= 8; i + n <= V).
@@ -126,19 +126,20 @@ __device__ __forceinline__ T wave_sum(T v) {
 
 // log2(e) / T, finite.
 __device__ __forceinline__ float exponent_scale(float T) {
-    return fminf(fminf(1.f / T, 3.402823466e38f) * kLog2e, 3.402823466e38f);
+    return fminf(fminf(1.f / T, kMaxFloat) * kLog2e, kMaxFloat);
 }
 
-// One slice's state: m, S, A in units of ln 2, and how many ids come before
-// the token.
+// One slice's state: m, S, A in units of ln 2, how many ids come before the
+// token, and the token's logit (the same in every slice of a row).
 struct Slice {
     float m, S, A;
     int before;
+    float lt;
 };
 
 struct LogprobsWs {
-    Slice* part;      // [B][slices]
     uint64_t* best;   // [B][slices][n_top] keys, best first, 0 past the last
+    Slice* part;      // [B][slices]
 };
 
 __device__ __forceinline__ void write_row(const LogprobsArgs& a, int b, float T, float m, float S,
@@ -193,93 +194,98 @@ __device__ __forceinline__ uint32_t nth_largest(const uint32_t (&k)[4], int n, i
 }
 
 // Best alternatives of a slice held in registers.  The n-th largest of the
-// threads' maxima bounds the n-th largest element from below, and only
-// threads that reach it hold elements that do: about n elements are
-// collected, ranked by counting and written best first.  Where equal values
-// make the collection overflow, only the threads of the lowest ids among the
-// tied ones count: n threads, n E elements at most.
-template <int DT, int E>
+// threads' maxima bounds the n-th largest element from below, and every element
+// of the answer lies in one of n threads: those with a maximum above the bound
+// and, of those that tie with it, the ones whose first equal id is lowest (n
+// ids that come before any other thread's are theirs).  These n threads leave
+// their elements in LDS; the ones that reach the bound (about n) are collected,
+// ranked by counting and written best first.
+template <int E>
 struct TopShared {
     float tmax[kLpThreads];
+    float value[kMaxAlternatives][E];
+    int owner[kMaxAlternatives];
+    uint64_t key[kMaxAlternatives * E];
     int first[kLpThreads];
-    uint64_t key[kCandidates];
-    int count;
-    float bound;
-    int id_limit;
+    int threads, count, tied, id_limit;
+    uint32_t bound;
 };
 
-template <int DT, int E, typename F, typename I>
-__device__ void best_of_slice(TopShared<DT, E>& s, const float (&x)[E], float tmax, I id_of, int n,
+template <int E, typename I, typename F>
+__device__ void best_of_slice(TopShared<E>& s, const float (&x)[E], float tmax, I id_of, int n,
                               F write) {
     const int t = threadIdx.x, lane = t & 63;
+    const uint32_t mine = float_to_ordered(tmax + 0.f);
     s.tmax[t] = tmax + 0.f;
-    if (t == 0) {
-        s.count = 0;
-        s.id_limit = 0x7FFFFFFF;
-    }
     __syncthreads();
-    uint32_t bound = 0;
-    int reach = 0;
     uint32_t k[4];
     if (t < 64) {
+        int reach = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) k[i] = float_to_ordered(s.tmax[lane + 64 * i]);
-        // (unmasked values only)
-        bound = max(nth_largest(k, n, reach), float_to_ordered(-INFINITY) + 1);
-        if (t == 0) s.bound = ordered_to_float(bound);
+        const uint32_t exact = nth_largest(k, n, reach);
+        const uint32_t least = float_to_ordered(-INFINITY) + 1;   // unmasked values only
+        if (t == 0) {
+            s.threads = s.count = 0;
+            s.bound = max(exact, least);
+            s.tied = reach > n && exact >= least;
+            s.id_limit = 0x7FFFFFFF;
+        }
     }
     __syncthreads();
-    auto collect = [&]() {
-        const float lo = s.bound;
-        const int limit = s.id_limit;
-        if (tmax >= lo) {
+    const uint32_t bound = s.bound;
+    const float lo = ordered_to_float(bound);
+    int first = 0x7FFFFFFF;
+    if (s.tied) {   // (the same for all threads)
+        if (mine == bound)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int id = id_of(e);
-                if (x[e] > lo || (x[e] == lo && id <= limit)) {
-                    const int at = atomicAdd(&s.count, 1);
-                    if (at < kCandidates) s.key[at] = pack_key(x[e] + 0.f, id);
-                }
-            }
-        }
-        __syncthreads();
-    };
-    collect();
-    if (s.count > kCandidates) {   // (the same for all threads)
-        int first = 0x7FFFFFFF;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (x[e] == s.bound) first = min(first, id_of(e));
+            for (int e = 0; e < E; ++e)
+                if (clean(x[e]) == lo) first = min(first, id_of(t, e));
         s.first[t] = first;
         __syncthreads();
         if (t < 64) {
             int above = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) above += __popcll(__ballot(k[i] > bound));
-            // the (n - above)-th lowest first id among the tied threads
-            uint32_t prefix = 0;
+            // the (n - above)-th lowest first id
+            uint32_t limit = 0;
             for (int bit = 30; bit >= 0; --bit) {
-                const uint32_t cand = prefix | ((1u << bit) - 1);
+                const uint32_t cand = limit | ((1u << bit) - 1);
                 int c = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     c += __popcll(__ballot((uint32_t)s.first[lane + 64 * i] <= cand));
-                if (c < n - above) prefix |= 1u << bit;
+                if (c < n - above) limit |= 1u << bit;
             }
-            if (t == 0) {
-                s.id_limit = (int)prefix;
-                s.count = 0;
-            }
+            if (t == 0) s.id_limit = (int)limit;
         }
         __syncthreads();
-        collect();
     }
-    const int c = min(s.count, kCandidates);
+    const bool pass = mine > bound || (mine == bound && (!s.tied || first <= s.id_limit));
+    const uint64_t who = __ballot(pass);
+    int slot = 0;
+    if (lane == 0 && who) slot = atomicAdd(&s.threads, __popcll(who));
+    slot = __shfl(slot, 0, 64) + __popcll(who & ((1ull << lane) - 1));
+    if (pass) {
+        s.owner[slot] = t;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.value[slot][e] = x[e];
+    }
+    __syncthreads();
+    const int held = s.threads * E;
+    for (int i = t; i < held; i += kLpThreads) {
+        const float v = s.value[i / E][i % E];
+        if (v >= lo)
+            s.key[atomicAdd(&s.count, 1)] =
+                pack_key(fminf(v, kMaxFloat) + 0.f, id_of(s.owner[i / E], i % E));
+    }
+    __syncthreads();
+    const int c = s.count;
     for (int i = t; i < c; i += kLpThreads) {
-        const uint64_t mine = s.key[i];
+        const uint64_t key = s.key[i];
         int r = 0;
-        for (int j = 0; j < c; ++j) r += s.key[j] > mine;
-        if (r < n) write(r, mine);
+        for (int j = 0; j < c; ++j) r += s.key[j] > key;
+        if (r < n) write(r, key);
     }
     for (int i = c + t; i < n; i += kLpThreads) write(i, (uint64_t)0);
 }
@@ -292,7 +298,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
     constexpr int N = Vec<DT>::kN;
     __shared__ float smax[kLpWaves], sS[kLpWaves], sA[kLpWaves];
     __shared__ int sbefore[kLpWaves];
-    __shared__ std::conditional_t<TOP, TopShared<DT, E>, char> top;
+    __shared__ std::conditional_t<TOP, TopShared<E>, char> top;
     const int n = valid_ids(a.V, a.n_valid, a.v_offset);
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -315,14 +321,17 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
         const float T = row_temp(a.temp, b, a.flags);
         int tok;
         const float lt = token_logit<DT>(a, allow_row, row, n, b, tok);
+        // NaN and +inf stay in x: every use below takes a NaN as masked (a
+        // maximum, a comparison and a median drop it) and +inf as kMaxFloat
         float x[E];
         float tmax = -INFINITY;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            x[e] = clean(raw[e / N].at(e % N));
+            x[e] = raw[e / N].at(e % N);
             if constexpr (MASKED) x[e] = (bits[e / N] >> (e % N)) & 1u ? x[e] : -INFINITY;
             tmax = fmaxf(tmax, x[e]);
         }
+        tmax = fminf(tmax, kMaxFloat);
         const float wmax = wave_max(tmax);
         if (lane == 0) smax[wave] = wmax;
         __syncthreads();
@@ -331,7 +340,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
         const float c = exponent_scale(T);
         const float from = m > -INFINITY ? m : 0.f;
         const bool has = lt > -INFINITY;
-        const float lt_below = has ? below(lt) : INFINITY, lt_over = has ? lt : INFINITY;
+        const float lt_below = has ? below(lt) : INFINITY;
+        const float lt_over = has && lt < kMaxFloat ? lt : INFINITY;
         float S = 0.f, A = 0.f;
         int before = 0;
 #pragma unroll
@@ -339,7 +349,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
             float S1 = 0.f, A1 = 0.f;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float d = fmaxf((x[j * N + e] - from) * c, kFloor);
+                const float d = __builtin_amdgcn_fmed3f((x[j * N + e] - from) * c, kFloor, 0.f);
                 const float p = __builtin_amdgcn_exp2f(d);
                 S1 += p;
                 A1 = fmaf(d, p, A1);
@@ -349,6 +359,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
             // ids before the token: wholly before it, those that reach its
             // logit; wholly behind it, those above
             const Chunk<DT> ch = chunk(j);
+            if (!a.rank) continue;
             if (ch.whole && (tok < ch.first || tok >= ch.first + 64 * N)) {
                 const float over = tok < ch.first ? lt_over : lt_below;
 #pragma unroll
@@ -356,7 +367,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
             } else if (has) {
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const float v = x[j * N + e];
+                    const float v = clean(x[j * N + e]);
                     before += v > lt || (v == lt && ch.id(e) < tok) ? 1 : 0;
                 }
             }
@@ -378,12 +389,15 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
             if (slices == 1)
                 write_row(a, b, T, m, S, A, before, lt, logS);
             else
-                ws.part[(size_t)b * slices + blockIdx.x] = Slice{m, S, A, before};
+                ws.part[(size_t)b * slices + blockIdx.x] = Slice{m, S, A, before, lt};
         }
         if constexpr (TOP) {
             uint64_t* out = ws.best + ((size_t)b * slices + blockIdx.x) * a.n_top;
-            auto id_of = [&](int e) { return chunk(e / N).id(e % N); };
-            best_of_slice<DT, E>(top, x, tmax, id_of, a.n_top, [&](int j, uint64_t key) {
+            auto id_of = [&](int thread, int e) {
+                return Chunk<DT>(base + (e / N * kLpWaves + (thread >> 6)) * 64 * N, n, thread & 63)
+                    .id(e % N);
+            };
+            best_of_slice<E>(top, x, tmax, id_of, a.n_top, [&](int j, uint64_t key) {
                 if (slices == 1)
                     write_best(a, b, j, key, T, m, logS);
                 else
@@ -396,21 +410,41 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
 
 // Joins the slices of a row.  Alternatives: with at least n slices the n-th
 // best of their first entries bounds the row's n-th best from below, and at
-// most n lists reach it.
+// most n lists reach it.  Bound by latency: everything a row needs is loaded
+// before the first use (rows of more than kJoinEntries entries read theirs
+// later).
+template <bool STAGED>
 __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs a, LogprobsWs ws,
                                                                    int slices) {
-    extern __shared__ __align__(16) uint64_t keys[];   // n_top * min(n_top, slices), heads
+    extern __shared__ __align__(16) uint64_t keys[];   // n_top min(n_top, slices), entries
+    constexpr int kPer = kJoinEntries / kLpThreads;
     __shared__ float smax[kLpWaves], sS[kLpWaves], sA[kLpWaves];
     __shared__ int sbefore[kLpWaves];
     __shared__ int count;
     __shared__ unsigned long long bound;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int n = a.n_top;
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const Slice* part = ws.part + (size_t)b * slices;
+        const uint64_t* best = ws.best + (size_t)b * slices * n;
+        uint64_t* entries = keys + n * min(n, slices);
+        uint64_t mine[kPer];
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (t + i * kLpThreads < slices * n) mine[i] = best[t + i * kLpThreads];
+        }
         const float T = row_temp(a.temp, b, a.flags);
-        const float c = exponent_scale(T);
-        float m = -INFINITY;
-        for (int i = t; i < slices; i += kLpThreads) m = fmaxf(m, part[i].m);
+        Slice p{-INFINITY, 0.f, 0.f, 0, 0.f};
+        if (t < slices) p = part[t];
+        const float lt = part[0].lt;
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (t + i * kLpThreads < slices * n) entries[t + i * kLpThreads] = mine[i];
+        }
+        float m = p.m;
+        for (int i = t + kLpThreads; i < slices; i += kLpThreads) m = fmaxf(m, part[i].m);
         m = wave_max(m);
         if (lane == 0) smax[wave] = m;
         if (t == 0) {
@@ -419,11 +453,12 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs 
         }
         __syncthreads();
         m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+        const float c = exponent_scale(T);
         const float from = m > -INFINITY ? m : 0.f;
         float S = 0.f, A = 0.f;
         int before = 0;
         for (int i = t; i < slices; i += kLpThreads) {
-            const Slice p = part[i];
+            if (i != t) p = part[i];
             const float d = fmaxf((p.m - from) * c, kFloor);
             const float w = __builtin_amdgcn_exp2f(d);
             S = fmaf(p.S, w, S);
@@ -438,54 +473,32 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs 
             sA[wave] = A;
             sbefore[wave] = before;
         }
+        const uint64_t* list = STAGED ? entries : best;
+        if (n > 0 && slices > n)
+            for (int i = t; i < slices; i += kLpThreads) {
+                const uint64_t head = list[(size_t)i * n];
+                int r = 0;
+                for (int j = 0; j < slices; ++j) r += list[(size_t)j * n] > head;
+                if (r == n - 1 && head) bound = head;   // (keys differ: one thread)
+            }
         __syncthreads();
         S = (sS[0] + sS[1]) + (sS[2] + sS[3]);
         A = (sA[0] + sA[1]) + (sA[2] + sA[3]);
         before = sbefore[0] + sbefore[1] + sbefore[2] + sbefore[3];
         const float logS = logf(S);
-        if (t == 0) {
-            // the token's logit once more (-inf: none to look at)
-            const int n = valid_ids(a.V, a.n_valid, a.v_offset);
-            const uint32_t* allow_row = a.allow ? a.allow + (size_t)b * ((a.V + 31) >> 5) : nullptr;
-            int tok;
-            float lt;
-            if (a.dtype == FS_F32)
-                lt = token_logit<FS_F32>(a, allow_row, static_cast<const float*>(a.logits) + (size_t)b * a.ld, n, b, tok);
-            else if (a.dtype == FS_BF16)
-                lt = token_logit<FS_BF16>(a, allow_row, static_cast<const __bf16*>(a.logits) + (size_t)b * a.ld, n, b, tok);
-            else
-                lt = token_logit<FS_F16>(a, allow_row, static_cast<const _Float16*>(a.logits) + (size_t)b * a.ld, n, b, tok);
-            write_row(a, b, T, m, S, A, before, lt, logS);
-        }
-        const int n = a.n_top;
+        if (t == 0) write_row(a, b, T, m, S, A, before, lt, logS);
         if (n > 0) {
-            const uint64_t* best = ws.best + (size_t)b * slices * n;
-            if (slices > n) {
-                uint64_t* heads = keys + n * n;
-                const bool staged = slices <= kHeads;
-                if (staged)
-                    for (int i = t; i < slices; i += kLpThreads) heads[i] = best[(size_t)i * n];
-                __syncthreads();
-                for (int i = t; i < slices; i += kLpThreads) {
-                    const uint64_t mine = best[(size_t)i * n];
-                    int r = 0;
-                    for (int j = 0; j < slices; ++j)
-                        r += (staged ? heads[j] : best[(size_t)j * n]) > mine;
-                    if (r == n - 1 && mine) bound = mine;   // (keys differ: one thread)
-                }
-            }
-            __syncthreads();
             const uint64_t lo = bound;
             for (int64_t i = t; i < (int64_t)slices * n; i += kLpThreads) {
-                const uint64_t k = best[i];
+                const uint64_t k = list[i];
                 if (k >= lo) keys[atomicAdd(&count, 1)] = k;
             }
             __syncthreads();
             for (int i = t; i < count; i += kLpThreads) {
-                const uint64_t mine = keys[i];
+                const uint64_t key = keys[i];
                 int r = 0;
-                for (int j = 0; j < count; ++j) r += keys[j] > mine;
-                if (r < n) write_best(a, b, r, mine, T, m, logS);
+                for (int j = 0; j < count; ++j) r += keys[j] > key;
+                if (r < n) write_best(a, b, r, key, T, m, logS);
             }
             for (int i = count + t; i < n; i += kLpThreads) write_best(a, b, i, 0, T, m, logS);
         }
@@ -615,8 +628,8 @@ int slice_elems(int B, int V, int cus) {
 
 LogprobsWs carve(const LogprobsArgs& a, void* ws, int slices) {
     LogprobsWs w;
-    w.part = static_cast<Slice*>(ws);
-    w.best = reinterpret_cast<uint64_t*>(w.part + (size_t)a.B * slices);
+    w.best = static_cast<uint64_t*>(ws);
+    w.part = reinterpret_cast<Slice*>(w.best + (size_t)a.B * slices * a.n_top);
     return w;
 }
 
@@ -663,9 +676,16 @@ hipError_t launch_logprobs(const LogprobsArgs& a, void* ws, int cus, hipStream_t
         launch_type<FS_F16>(a, w, slices, lng, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || slices == 1) return e;
-    // at most 40 KiB
-    const size_t lds = 8 * ((size_t)a.n_top * std::min(a.n_top, slices) + std::min(slices, kHeads));
-    hipLaunchKernelGGL(logprobs_join_kernel, dim3(a.B), dim3(kLpThreads), lds, stream, a, w, slices);
+    // at most 32 KiB of candidates and 16 KiB of entries
+    const int64_t entries = (int64_t)slices * a.n_top;
+    const bool staged = entries <= kJoinEntries;
+    const size_t lds = 8 * ((size_t)a.n_top * std::min(a.n_top, slices) + (staged ? entries : 0));
+    if (staged)
+        hipLaunchKernelGGL(logprobs_join_kernel<true>, dim3(a.B), dim3(kLpThreads), lds, stream, a,
+                           w, slices);
+    else
+        hipLaunchKernelGGL(logprobs_join_kernel<false>, dim3(a.B), dim3(kLpThreads), lds, stream, a,
+                           w, slices);
     return hipGetLastError();
 }
 
