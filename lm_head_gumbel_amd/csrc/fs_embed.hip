@@ -4,7 +4,7 @@
 // Both are bound by memory: a read and a write of [N, d], and for the gradient
 // one read of g and one write of dW.  The gradient sorts the tokens by id
 // (stable radix sort, so equal ids keep the order of n), cuts the sorted list
-// into chunks of kChunk, sums each chunk's runs of equal ids in FP32 and
+// into chunks, sums each chunk's runs of equal ids in FP32 and
 // writes the runs that lie inside a chunk straight to dW; runs that cross a
 // chunk's end leave partial rows, which a last kernel adds up in order.  The
 // order of every sum follows from the ids alone.
@@ -173,6 +173,29 @@ __device__ __forceinline__ void scan_digits(SortShared& s, uint32_t v) {
     __syncthreads();
 }
 
+// Few tokens: each finds its place by counting the keys before it.
+constexpr int kFew = 1024;
+__global__ __launch_bounds__(kEmThreads) void sort_few_kernel(const int32_t* ids, int N,
+                                                              int v_offset, int V,
+                                                              uint32_t* out_key,
+                                                              uint32_t* out_pos) {
+    __shared__ __align__(16) uint32_t key[kFew];
+    for (int i = threadIdx.x; i < kFew; i += kEmThreads)
+        key[i] = i < N ? row_key_of(ids[i], v_offset, V) : ~0u;
+    __syncthreads();
+    const int n = blockIdx.x * kEmThreads + threadIdx.x;
+    if (n >= N) return;
+    const uint32_t mine = key[n];
+    int at = 0;
+    for (int i = 0; i < N; i += 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(key + i);
+        at += (k.x < mine || (k.x == mine && i < n)) + (k.y < mine || (k.y == mine && i + 1 < n)) +
+              (k.z < mine || (k.z == mine && i + 2 < n)) + (k.w < mine || (k.w == mine && i + 3 < n));
+    }
+    out_key[at] = mine;
+    out_pos[at] = n;
+}
+
 // One tile: the whole sort in LDS.
 __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const int32_t* ids, int N,
                                                                   int v_offset, int V, int passes,
@@ -289,7 +312,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortPass a,
 // ---------------------------------------------------------------------------
 // sums of the runs of equal ids
 // ---------------------------------------------------------------------------
-constexpr int kChunk = 32;      // sorted tokens per chunk
+// Sorted tokens per chunk: few where there are few tokens (a chunk's rows are
+// read kAhead at a time, one latency each), more where partial rows would
+// cost traffic.
+constexpr int kAhead = 8;
+constexpr int kMaxChunk = 32;
+int chunk_for(int N) { return N <= 4096 ? kAhead : kMaxChunk; }
 constexpr int kZeroRows = 64;   // rows of dW that one workgroup fills with zeros
 
 struct SumArgs {
@@ -299,10 +327,12 @@ struct SumArgs {
     void* dW;
     float* part;           // [chunks][2][d]: head (a run from before), tail (a run going on)
     int N, d, V;
+    int chunk;             // sorted tokens per chunk
     float scale;
     int accumulate;
     int lanes;             // threads per chunk and column block (a power of two)
     int col_blocks;
+    int zero_lanes;        // threads per row that fills with zeros (a power of two)
     int sum_wgs;           // workgroups that sum; the others fill with zeros
 };
 
@@ -345,13 +375,13 @@ __device__ void zero_rows(const SumArgs& a, uint32_t row0) {
     }
     __syncthreads();
     const float zero[N] = {};
-    for (int w = 0; w < kZeroRows / 32; ++w)
-        for (uint32_t left = ~named[w]; left; left &= left - 1) {
-            const uint32_t row = row0 + w * 32 + __builtin_ctz(left);
-            if (row >= (uint32_t)a.V) break;
-            O* out = static_cast<O*>(a.dW) + (size_t)row * a.d;
-            for (int k = t * N; k < a.d; k += kEmThreads * N) store_row<DO, N>(out, k, a.d, zero);
-        }
+    for (int r = t / a.zero_lanes; r < kZeroRows; r += kEmThreads / a.zero_lanes) {
+        const uint32_t row = row0 + r;
+        if (row >= (uint32_t)a.V || ((named[r / 32] >> (r % 32)) & 1u)) continue;
+        O* out = static_cast<O*>(a.dW) + (size_t)row * a.d;
+        for (int k = t % a.zero_lanes * N; k < a.d; k += a.zero_lanes * N)
+            store_row<DO, N>(out, k, a.d, zero);
+    }
     __syncthreads();   // before the next rows' marks
 }
 // Workgroup i of the wgs behind a kernel's own that fill with zeros.
@@ -376,25 +406,24 @@ __global__ __launch_bounds__(kEmThreads) void embed_sum_kernel(SumArgs a) {
     const int k = ((int)(blockIdx.x % a.col_blocks) * a.lanes + lane) * N;
     // the chunks' rows and tokens, with the row before the first and the one
     // behind the last (none: ~0)
-    extern __shared__ uint32_t list[];   // per kChunk + 2 rows, per kChunk tokens
-    uint32_t* toks = list + per * kChunk + 2;
-    const int64_t base = c0 * kChunk;
-    for (int i = threadIdx.x; i < per * kChunk + 2; i += kEmThreads) {
+    extern __shared__ uint32_t list[];   // per a.chunk + 2 rows, per a.chunk tokens
+    uint32_t* toks = list + per * a.chunk + 2;
+    const int64_t base = c0 * a.chunk;
+    for (int i = threadIdx.x; i < per * a.chunk + 2; i += kEmThreads) {
         const int64_t at = base + i - 1;
         list[i] = at >= 0 && at < a.N ? a.key[at] : ~0u;
     }
-    for (int i = threadIdx.x; i < per * kChunk; i += kEmThreads)
+    for (int i = threadIdx.x; i < per * a.chunk; i += kEmThreads)
         toks[i] = base + i < a.N ? a.pos[base + i] : 0;
     __syncthreads();
     const int64_t c = c0 + sub;
-    if (c * kChunk >= a.N || k >= a.d) return;
-    const uint32_t* rows = list + sub * kChunk + 1;
-    const uint32_t* tok = toks + sub * kChunk;
-    const int len = (int)min((int64_t)kChunk, a.N - c * kChunk);
+    if (c * a.chunk >= a.N || k >= a.d) return;
+    const uint32_t* rows = list + sub * a.chunk + 1;
+    const uint32_t* tok = toks + sub * a.chunk;
+    const int len = (int)min((int64_t)a.chunk, a.N - c * a.chunk);
     const E* g = static_cast<const E*>(a.g);
     float acc[N] = {};
     bool head = rows[-1] == rows[0];   // the first run began in an earlier chunk
-    constexpr int kAhead = 8;          // rows of g in flight
     for (int i = 0; i < len; i += kAhead) {
         float x[kAhead][N];
 #pragma unroll
@@ -434,10 +463,10 @@ __global__ __launch_bounds__(kEmThreads) void embed_join_kernel(SumArgs a, int c
     const int64_t c = (int64_t)(blockIdx.x / a.col_blocks) * per + sub;
     const int k = ((int)(blockIdx.x % a.col_blocks) * a.lanes + lane) * N;
     if (c + 1 >= chunks || k >= a.d) return;
-    const int64_t next = (c + 1) * kChunk;   // the next chunk's first token
+    const int64_t next = (c + 1) * a.chunk;   // the next chunk's first token
     const uint32_t row = a.key[next];
     if (row >= (uint32_t)a.V || a.key[next - 1] != row) return;   // no run crosses
-    if (c > 0 && a.key[next - kChunk - 1] == row) return;         // it began earlier
+    if (c > 0 && a.key[next - a.chunk - 1] == row) return;         // it began earlier
     auto load_part = [&](int64_t chunk, int tail, float* x) {
         const float* p = a.part + ((size_t)chunk * 2 + tail) * a.d;
         load_row<FS_F32>(p, k, a.d, x);
@@ -445,14 +474,13 @@ __global__ __launch_bounds__(kEmThreads) void embed_join_kernel(SumArgs a, int c
     };
     float acc[N];
     load_part(c, 1, acc);
-    constexpr int kAhead = 8;
     bool more = true;
     for (int64_t j = c + 1; more; j += kAhead) {
         float x[kAhead][N];
         bool on[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            on[u] = j + u < chunks && a.key[(j + u) * kChunk] == row;
+            on[u] = j + u < chunks && a.key[(j + u) * a.chunk] == row;
             if (on[u]) load_part(j + u, 0, x[u]);
         }
 #pragma unroll
@@ -487,7 +515,7 @@ GradWs grad_ws(int N, int d) {
         return r;
     };
     const size_t tiles = ((size_t)N + kTile - 1) / kTile;
-    const size_t chunks = ((size_t)N + kChunk - 1) / kChunk;
+    const size_t chunks = ((size_t)N + chunk_for(N) - 1) / chunk_for(N);
     for (int i = 0; i < 2; ++i) {
         w.key[i] = take((size_t)N * 4);
         w.pos[i] = take((size_t)N * 4);
@@ -504,12 +532,15 @@ hipError_t launch_sums(const EmbedGradArgs& a, SumArgs s, hipStream_t stream) {
     const int vecs = (a.d + N - 1) / N;
     s.lanes = std::max(4, lanes_for(vecs));   // (at most 64 chunks' lists per workgroup)
     s.col_blocks = (vecs + s.lanes - 1) / s.lanes;
-    const int chunks = (a.N + kChunk - 1) / kChunk;
+    s.chunk = chunk_for(a.N);
+    const int chunks = (a.N + s.chunk - 1) / s.chunk;
     const int per = kEmThreads / s.lanes;
     s.sum_wgs = (chunks + per - 1) / per * s.col_blocks;
     const int zero_wgs =
         a.accumulate ? 0 : (int)std::min(((int64_t)a.V + kZeroRows - 1) / kZeroRows, kMaxGridX);
-    const size_t lds = 4 * (size_t)(2 * per * kChunk + 2);   // at most 16 KiB + 8
+    const int zn = 16 / (int)sizeof(typename Elem<DO>::type);
+    s.zero_lanes = lanes_for((a.d + zn - 1) / zn);
+    const size_t lds = 4 * (size_t)(2 * per * s.chunk + 2);   // at most 16 KiB + 8
     const int here = chunks < 2 ? zero_wgs : 0;
     if (s.sum_wgs + here > 0)
         hipLaunchKernelGGL((embed_sum_kernel<DT, DO>), dim3(s.sum_wgs + here), dim3(kEmThreads),
@@ -547,7 +578,10 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, void* ws, hipStream_t strea
     int passes = 1;
     while (passes * kDigitBits < 32 && ((uint32_t)a.V >> (passes * kDigitBits)) != 0) ++passes;
     int at = 0;   // the arrays that hold the sorted tokens
-    if (a.N > 0 && a.N <= kTile) {
+    if (a.N > 0 && a.N <= kFew) {
+        hipLaunchKernelGGL(sort_few_kernel, dim3((a.N + kEmThreads - 1) / kEmThreads), dim3(kEmThreads), 0,
+                           stream, a.ids, a.N, a.v_offset, a.V, u32(lay.key[0]), u32(lay.pos[0]));
+    } else if (a.N > 0 && a.N <= kTile) {
         hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSortThreads), 0, stream, a.ids, a.N,
                            a.v_offset, a.V, passes, u32(lay.key[0]), u32(lay.pos[0]));
     } else if (a.N > 0) {

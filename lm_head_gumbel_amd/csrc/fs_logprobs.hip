@@ -342,39 +342,59 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
         const bool has = lt > -INFINITY;
         const float lt_below = has ? below(lt) : INFINITY;
         const float lt_over = has && lt < kMaxFloat ? lt : INFINITY;
+        // (a wave whose largest is below the token has none before it)
+        const bool count = a.rank && has && wmax >= lt;
         float S = 0.f, A = 0.f;
-        int before = 0;
+        auto add = [&](auto d_of) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < E / N; ++j) {
-            float S1 = 0.f, A1 = 0.f;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float d = __builtin_amdgcn_fmed3f((x[j * N + e] - from) * c, kFloor, 0.f);
-                const float p = __builtin_amdgcn_exp2f(d);
-                S1 += p;
-                A1 = fmaf(d, p, A1);
-            }
-            S += S1;
-            A += A1;
-            // ids before the token: wholly before it, those that reach its
-            // logit; wholly behind it, those above
-            const Chunk<DT> ch = chunk(j);
-            if (!a.rank) continue;
-            if (ch.whole && (tok < ch.first || tok >= ch.first + 64 * N)) {
-                const float over = tok < ch.first ? lt_over : lt_below;
-#pragma unroll
-                for (int e = 0; e < N; ++e) before += x[j * N + e] > over ? 1 : 0;
-            } else if (has) {
+            for (int j = 0; j < E / N; ++j) {
+                float S1 = 0.f, A1 = 0.f;
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const float v = clean(x[j * N + e]);
-                    before += v > lt || (v == lt && ch.id(e) < tok) ? 1 : 0;
+                    const float d = d_of(x[j * N + e]);
+                    const float p = __builtin_amdgcn_exp2f(d);
+                    S1 += p;
+                    A1 = fmaf(d, p, A1);
+                }
+                S += S1;
+                A += A1;
+            }
+        };
+        const float ref = from * c;
+        if (fabsf(ref) < 65536.f) {
+            // Exponents (v - m) c as one multiply-add, v c - ref: all of them
+            // are off by the same eta = ref - m c (below 2^-8), which the sums
+            // take back.
+            const float eta = fmaf(-from, c, ref);
+            add([&](float v) { return __builtin_amdgcn_fmed3f(fmaf(v, c, -ref), kFloor, -eta); });
+            const float back = __builtin_amdgcn_exp2f(eta);
+            A = fmaf(eta, S, A) * back;
+            S *= back;
+        } else {
+            add([&](float v) { return __builtin_amdgcn_fmed3f((v - from) * c, kFloor, 0.f); });
+        }
+        // ids before the token: in chunks wholly before it, those that reach
+        // its logit; in chunks wholly behind it, those above
+        int before = 0, mixed = 0;   // of the wave, of the lane
+        if (count)
+#pragma unroll
+            for (int j = 0; j < E / N; ++j) {
+                const Chunk<DT> ch = chunk(j);
+                if (ch.whole && (tok < ch.first || tok >= ch.first + 64 * N)) {
+                    const float over = tok < ch.first ? lt_over : lt_below;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) before += __popcll(__ballot(x[j * N + e] > over));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float v = clean(x[j * N + e]);
+                        mixed += v > lt || (v == lt && ch.id(e) < tok) ? 1 : 0;
+                    }
                 }
             }
-        }
         S = wave_sum(S);
         A = wave_sum(A);
-        before = wave_sum(before);
+        before += wave_sum(mixed);
         if (lane == 0) {
             sS[wave] = S;
             sA[wave] = A;
@@ -622,7 +642,7 @@ int slice_elems(int B, int V, int cus) {
     // long slices once they fill the chip
     const int64_t one = (int64_t)kLpThreads * kLpLong;
     if (V <= kLpThreads * kLpShort) return kLpThreads * kLpShort;
-    if (V <= one || (int64_t)B * ((V + one - 1) / one) >= 2 * cus) return (int)one;
+    if (V <= one || (int64_t)B * ((V + one - 1) / one) >= 8 * cus) return (int)one;
     return kLpThreads * kLpShort;
 }
 
