@@ -112,16 +112,38 @@ __device__ __forceinline__ void load_chunk(const Chunk<DT>& c,
     }
 }
 
+// Reductions of a wave in its vector registers (data-parallel primitives: a
+// row of 16 lanes in four steps, the rows in two), the same in every lane.
+template <int CTRL, int ROWS, typename T>
+__device__ __forceinline__ T lanes_from(T v, T identity) {
+    static_assert(sizeof(T) == 4, "one register");
+    return __builtin_bit_cast(
+        T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, identity), __builtin_bit_cast(int, v),
+                                       CTRL, ROWS, 0xF, false));
+}
+template <typename T, typename F>
+__device__ __forceinline__ T wave_reduce(T v, T identity, F op) {
+    v = op(v, lanes_from<0x111, 0xF>(v, identity));   // row_shr 1, 2, 4, 8
+    v = op(v, lanes_from<0x112, 0xF>(v, identity));
+    v = op(v, lanes_from<0x114, 0xF>(v, identity));
+    v = op(v, lanes_from<0x118, 0xF>(v, identity));
+    v = op(v, lanes_from<0x142, 0xA>(v, identity));   // row_bcast 15, 31
+    v = op(v, lanes_from<0x143, 0xC>(v, identity));
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-    return v;
+    return wave_reduce(v, -INFINITY, [](float x, float y) { return fmaxf(x, y); });
 }
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-    return v;
+    return wave_reduce(v, (T)0, [](T x, T y) { return x + y; });
+}
+// The larger of three, without the quieting of signalling NaNs that fmaxf
+// brings (one operation per element).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
 }
 
 // log2(e) / T, finite.
@@ -175,16 +197,17 @@ __device__ __forceinline__ float below(float x) {
     return x == 0.f ? __uint_as_float(0x80000001u) : ordered_to_float(float_to_ordered(x) - 1);
 }
 
-// The n-th largest of 256 keys k[4] (one wave, four a lane), or a smaller
-// value that at least n keys reach; sure == n: exactly n keys reach it.
-__device__ __forceinline__ uint32_t nth_largest(const uint32_t (&k)[4], int n, int& reach) {
+// The n-th largest of the wave's 64 K keys (K a lane), or a smaller value that
+// exactly n keys reach; reach: how many do.
+template <int K>
+__device__ __forceinline__ uint32_t nth_largest(const uint32_t (&k)[K], int n, int& reach) {
     uint32_t prefix = 0;
-    reach = kLpThreads;
+    reach = 64 * K;
     for (int bit = 31; bit >= 0 && reach != n; --bit) {
         const uint32_t cand = prefix | (1u << bit);
         int c = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c += __popcll(__ballot(k[i] >= cand));
+        for (int i = 0; i < K; ++i) c += __popcll(__ballot(k[i] >= cand));
         if (c >= n) {
             prefix = cand;
             reach = c;
@@ -192,28 +215,87 @@ __device__ __forceinline__ uint32_t nth_largest(const uint32_t (&k)[4], int n, i
     }
     return prefix;
 }
+// The smallest id (or larger) that at least n of the 256 ids reach from below.
+__device__ __forceinline__ int nth_lowest(const int* ids, int n) {
+    const int lane = threadIdx.x & 63;
+    uint32_t limit = 0;
+    for (int bit = 30; bit >= 0; --bit) {
+        const uint32_t cand = limit | ((1u << bit) - 1);
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kLpThreads / 64; ++i)
+            c += __popcll(__ballot((uint32_t)ids[lane + 64 * i] <= cand));
+        if (c < n) limit |= 1u << bit;
+    }
+    return (int)limit;
+}
 
-// Best alternatives of a slice held in registers.  The n-th largest of the
-// threads' maxima bounds the n-th largest element from below, and every element
-// of the answer lies in one of n threads: those with a maximum above the bound
-// and, of those that tie with it, the ones whose first equal id is lowest (n
-// ids that come before any other thread's are theirs).  These n threads leave
-// their elements in LDS; the ones that reach the bound (about n) are collected,
-// ranked by counting and written best first.
+// Best alternatives of a slice held in registers.  A value that at least n
+// threads' maxima reach bounds the n-th largest element from below, and only
+// threads that reach it hold elements of the answer.  Each wave offers the
+// ceil(n / 4)-th largest of its lanes' maxima, and the lowest of the four
+// offers is such a value: the threads that reach it (somewhat over n) leave
+// their elements in LDS, the elements that reach it are collected, ranked by
+// counting and written best first.  Where more than kHeld threads reach it
+// (values in the order of the ids, many equal values), it is raised to the
+// exact n-th largest maximum, and of the threads that tie with that only those
+// count whose first equal id is lowest: n threads in all.  (An element of the
+// answer in another tied thread would have the n - above first ids of those
+// and the above larger maxima before it.)
+constexpr int kHeld = 96;    // at least kMaxAlternatives
+constexpr int kKeys = 512;   // collected elements that are compacted
 template <int E>
 struct TopShared {
+    float value[kHeld][E];
+    uint64_t key[kKeys];
+    int owner[kHeld];
     float tmax[kLpThreads];
-    float value[kMaxAlternatives][E];
-    int owner[kMaxAlternatives];
-    uint64_t key[kMaxAlternatives * E];
     int first[kLpThreads];
+    uint32_t offer[kLpWaves];
     int threads, count, tied, id_limit;
     uint32_t bound;
 };
 
-template <int E, typename I, typename F>
-__device__ void best_of_slice(TopShared<E>& s, const float (&x)[E], float tmax, I id_of, int n,
-                              F write) {
+// This wave's offer, before the barrier that ends the maxima.
+template <int E>
+__device__ __forceinline__ void offer_bound(TopShared<E>& s, float tmax, int n) {
+    const uint32_t k[1] = {float_to_ordered(tmax + 0.f)};
+    int reach;
+    const uint32_t b = nth_largest(k, (n + kLpWaves - 1) / kLpWaves, reach);
+    if ((threadIdx.x & 63) == 0) s.offer[threadIdx.x >> 6] = b;
+    if (threadIdx.x == 0) s.threads = s.count = 0;
+}
+
+// A passing thread's elements to LDS.
+template <int E>
+__device__ __forceinline__ void hold(TopShared<E>& s, const float (&x)[E], bool pass) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t who = __ballot(pass);
+    int slot = 0;
+    if (lane == 0 && who) slot = atomicAdd(&s.threads, __popcll(who));
+    slot = __builtin_amdgcn_readfirstlane(slot) + __popcll(who & ((1ull << lane) - 1));
+    if (pass && slot < kHeld) {
+        s.owner[slot] = threadIdx.x;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.value[slot][e] = x[e];
+    }
+}
+
+// After that barrier; the next barrier ends it.
+template <int E>
+__device__ __forceinline__ uint32_t hold_offers(TopShared<E>& s, const float (&x)[E], float tmax) {
+    uint32_t bound = s.offer[0];
+#pragma unroll
+    for (int w = 1; w < kLpWaves; ++w) bound = min(bound, s.offer[w]);
+    bound = max(bound, float_to_ordered(-INFINITY) + 1);   // unmasked values only
+    hold(s, x, float_to_ordered(tmax + 0.f) >= bound);
+    return bound;
+}
+
+// The exact bound, where the offers hold too many threads.
+template <int E, typename I>
+__device__ __forceinline__ uint32_t hold_exact(TopShared<E>& s, const float (&x)[E],
+                                                         float tmax, I id_of, int n) {
     const int t = threadIdx.x, lane = t & 63;
     const uint32_t mine = float_to_ordered(tmax + 0.f);
     s.tmax[t] = tmax + 0.f;
@@ -224,9 +306,9 @@ __device__ void best_of_slice(TopShared<E>& s, const float (&x)[E], float tmax, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) k[i] = float_to_ordered(s.tmax[lane + 64 * i]);
         const uint32_t exact = nth_largest(k, n, reach);
-        const uint32_t least = float_to_ordered(-INFINITY) + 1;   // unmasked values only
+        const uint32_t least = float_to_ordered(-INFINITY) + 1;
         if (t == 0) {
-            s.threads = s.count = 0;
+            s.threads = 0;
             s.bound = max(exact, least);
             s.tied = reach > n && exact >= least;
             s.id_limit = 0x7FFFFFFF;
@@ -237,63 +319,72 @@ __device__ void best_of_slice(TopShared<E>& s, const float (&x)[E], float tmax, 
     const float lo = ordered_to_float(bound);
     int first = 0x7FFFFFFF;
     if (s.tied) {   // (the same for all threads)
+        int me = t;
+        asm volatile("" : "+v"(me));   // the ids are formed here only
         if (mine == bound)
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (clean(x[e]) == lo) first = min(first, id_of(t, e));
+                if (clean(x[e]) == lo) first = min(first, id_of(me, e));
         s.first[t] = first;
         __syncthreads();
         if (t < 64) {
             int above = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) above += __popcll(__ballot(k[i] > bound));
-            // the (n - above)-th lowest first id
-            uint32_t limit = 0;
-            for (int bit = 30; bit >= 0; --bit) {
-                const uint32_t cand = limit | ((1u << bit) - 1);
-                int c = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    c += __popcll(__ballot((uint32_t)s.first[lane + 64 * i] <= cand));
-                if (c < n - above) limit |= 1u << bit;
-            }
-            if (t == 0) s.id_limit = (int)limit;
+            const int limit = nth_lowest(s.first, n - above);
+            if (t == 0) s.id_limit = limit;
         }
         __syncthreads();
     }
-    const bool pass = mine > bound || (mine == bound && (!s.tied || first <= s.id_limit));
-    const uint64_t who = __ballot(pass);
-    int slot = 0;
-    if (lane == 0 && who) slot = atomicAdd(&s.threads, __popcll(who));
-    slot = __shfl(slot, 0, 64) + __popcll(who & ((1ull << lane) - 1));
-    if (pass) {
-        s.owner[slot] = t;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s.value[slot][e] = x[e];
-    }
+    hold(s, x, mine > bound || (mine == bound && (!s.tied || first <= s.id_limit)));
     __syncthreads();
+    return bound;
+}
+
+// The held elements that reach the bound, ranked.
+template <int E, typename I, typename F>
+__device__ __forceinline__ void write_best_of(TopShared<E>& s, uint32_t bound, I id_of, int n,
+                                              F write) {
+    const int t = threadIdx.x;
+    const float lo = ordered_to_float(bound);
     const int held = s.threads * E;
-    for (int i = t; i < held; i += kLpThreads) {
+    auto key_of = [&](int i) {   // 0: below the bound
         const float v = s.value[i / E][i % E];
-        if (v >= lo)
-            s.key[atomicAdd(&s.count, 1)] =
-                pack_key(fminf(v, kMaxFloat) + 0.f, id_of(s.owner[i / E], i % E));
+        return v >= lo ? pack_key(fminf(v, kMaxFloat) + 0.f, id_of(s.owner[i / E], i % E))
+                       : (uint64_t)0;
+    };
+    for (int i = t; i < held; i += kLpThreads) {
+        const uint64_t key = key_of(i);
+        if (key) {
+            const int at = atomicAdd(&s.count, 1);
+            if (at < kKeys) s.key[at] = key;
+        }
     }
     __syncthreads();
     const int c = s.count;
-    for (int i = t; i < c; i += kLpThreads) {
-        const uint64_t key = s.key[i];
-        int r = 0;
-        for (int j = 0; j < c; ++j) r += s.key[j] > key;
-        if (r < n) write(r, key);
+    if (c <= kKeys) {
+        for (int i = t; i < c; i += kLpThreads) {
+            const uint64_t key = s.key[i];
+            int r = 0;
+            for (int j = 0; j < c; ++j) r += s.key[j] > key;
+            if (r < n) write(r, key);
+        }
+    } else {   // (many of the best in few threads)
+        for (int i = t; i < held; i += kLpThreads) {
+            const uint64_t key = key_of(i);
+            if (!key) continue;
+            int r = 0;
+            for (int j = 0; j < held && r < n; ++j) r += key_of(j) > key;
+            if (r < n) write(r, key);
+        }
     }
     for (int i = c + t; i < n; i += kLpThreads) write(i, (uint64_t)0);
 }
 
 // One slice of kLpThreads E elements of a row.
 template <int DT, int E, bool MASKED, bool TOP>
-__global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, LogprobsWs ws,
-                                                              int slices) {
+__global__ __launch_bounds__(kLpThreads, 7) void logprobs_kernel(LogprobsArgs a, LogprobsWs ws,
+                                                                 int slices) {
     typedef typename Elem<DT>::type T_;
     constexpr int N = Vec<DT>::kN;
     __shared__ float smax[kLpWaves], sS[kLpWaves], sA[kLpWaves];
@@ -313,14 +404,14 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
         };
         const T_* row = static_cast<const T_*>(a.logits) + (size_t)b * a.ld;
         const uint32_t* allow_row = a.allow ? a.allow + (size_t)b * ((a.V + 31) >> 5) : nullptr;
+        const float T = row_temp(a.temp, b, a.flags);
+        int tok;
+        const float lt = token_logit<DT>(a, allow_row, row, n, b, tok);
         Vec<DT> raw[E / N];
         uint32_t bits[E / N];
 #pragma unroll
         for (int j = 0; j < E / N; ++j)
             load_chunk<DT, MASKED>(chunk(j), row, allow_row, n, raw[j], bits[j]);
-        const float T = row_temp(a.temp, b, a.flags);
-        int tok;
-        const float lt = token_logit<DT>(a, allow_row, row, n, b, tok);
         // NaN and +inf stay in x: every use below takes a NaN as masked (a
         // maximum, a comparison and a median drop it) and +inf as kMaxFloat
         float x[E];
@@ -329,13 +420,22 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
         for (int e = 0; e < E; ++e) {
             x[e] = raw[e / N].at(e % N);
             if constexpr (MASKED) x[e] = (bits[e / N] >> (e % N)) & 1u ? x[e] : -INFINITY;
-            tmax = fmaxf(tmax, x[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < E; e += 2) tmax = max3(tmax, x[e], x[e + 1]);
+        if (__any(tmax != tmax)) {   // (a signalling NaN: the maximum takes it over)
+            tmax = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < E; ++e) tmax = fmaxf(tmax, clean(x[e]));
         }
         tmax = fminf(tmax, kMaxFloat);
         const float wmax = wave_max(tmax);
         if (lane == 0) smax[wave] = wmax;
+        if constexpr (TOP) offer_bound<E>(top, tmax, a.n_top);
         __syncthreads();
         const float m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+        uint32_t bound = 0;
+        if constexpr (TOP) bound = hold_offers<E>(top, x, tmax);
 
         const float c = exponent_scale(T);
         const float from = m > -INFINITY ? m : 0.f;
@@ -345,33 +445,18 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
         // (a wave whose largest is below the token has none before it)
         const bool count = a.rank && has && wmax >= lt;
         float S = 0.f, A = 0.f;
-        auto add = [&](auto d_of) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < E / N; ++j) {
-                float S1 = 0.f, A1 = 0.f;
+        for (int j = 0; j < E / N; ++j) {
+            float S1 = 0.f, A1 = 0.f;
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float d = d_of(x[j * N + e]);
-                    const float p = __builtin_amdgcn_exp2f(d);
-                    S1 += p;
-                    A1 = fmaf(d, p, A1);
-                }
-                S += S1;
-                A += A1;
+            for (int e = 0; e < N; ++e) {
+                const float d = __builtin_amdgcn_fmed3f((x[j * N + e] - from) * c, kFloor, 0.f);
+                const float p = __builtin_amdgcn_exp2f(d);
+                S1 += p;
+                A1 = fmaf(d, p, A1);
             }
-        };
-        const float ref = from * c;
-        if (fabsf(ref) < 65536.f) {
-            // Exponents (v - m) c as one multiply-add, v c - ref: all of them
-            // are off by the same eta = ref - m c (below 2^-8), which the sums
-            // take back.
-            const float eta = fmaf(-from, c, ref);
-            add([&](float v) { return __builtin_amdgcn_fmed3f(fmaf(v, c, -ref), kFloor, -eta); });
-            const float back = __builtin_amdgcn_exp2f(eta);
-            A = fmaf(eta, S, A) * back;
-            S *= back;
-        } else {
-            add([&](float v) { return __builtin_amdgcn_fmed3f((v - from) * c, kFloor, 0.f); });
+            S += S1;
+            A += A1;
         }
         // ids before the token: in chunks wholly before it, those that reach
         // its logit; in chunks wholly behind it, those above
@@ -417,7 +502,11 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
                 return Chunk<DT>(base + (e / N * kLpWaves + (thread >> 6)) * 64 * N, n, thread & 63)
                     .id(e % N);
             };
-            best_of_slice<E>(top, x, tmax, id_of, a.n_top, [&](int j, uint64_t key) {
+            if (top.threads > kHeld) {   // (the same for all threads)
+                __syncthreads();
+                bound = hold_exact<E>(top, x, tmax, id_of, a.n_top);
+            }
+            write_best_of<E>(top, bound, id_of, a.n_top, [&](int j, uint64_t key) {
                 if (slices == 1)
                     write_best(a, b, j, key, T, m, logS);
                 else
@@ -428,9 +517,10 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a, Lo
     }
 }
 
-// Joins the slices of a row.  Alternatives: with at least n slices the n-th
+// Joins the slices of a row.  Alternatives: with more than n slices the n-th
 // best of their first entries bounds the row's n-th best from below, and at
-// most n lists reach it.  Bound by latency: everything a row needs is loaded
+// most n lists reach it; with fewer, the n-th largest of the threads' largest
+// entries bounds it.  Bound by latency: everything a row needs is loaded
 // before the first use (rows of more than kJoinEntries entries read theirs
 // later).
 template <bool STAGED>
@@ -442,6 +532,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs 
     __shared__ int sbefore[kLpWaves];
     __shared__ int count;
     __shared__ unsigned long long bound;
+    __shared__ uint32_t tbest[kLpThreads];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int n = a.n_top;
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -462,6 +553,18 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs 
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 if (t + i * kLpThreads < slices * n) entries[t + i * kLpThreads] = mine[i];
+        }
+        if (n > 0 && slices <= n) {
+            uint32_t most = 0;
+            if constexpr (STAGED) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (t + i * kLpThreads < slices * n) most = max(most, (uint32_t)(mine[i] >> 32));
+            } else {
+                for (int64_t i = t; i < (int64_t)slices * n; i += kLpThreads)
+                    most = max(most, (uint32_t)(best[i] >> 32));
+            }
+            tbest[t] = most;
         }
         float m = p.m;
         for (int i = t + kLpThreads; i < slices; i += kLpThreads) m = fmaxf(m, part[i].m);
@@ -501,6 +604,14 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs 
                 for (int j = 0; j < slices; ++j) r += list[(size_t)j * n] > head;
                 if (r == n - 1 && head) bound = head;   // (keys differ: one thread)
             }
+        if (n > 0 && slices <= n && t < 64) {
+            uint32_t k[4];
+            int reach;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = tbest[lane + 64 * i];
+            const uint32_t v = nth_largest(k, n, reach);
+            if (t == 0 && v) bound = (unsigned long long)v << 32;
+        }
         __syncthreads();
         S = (sS[0] + sS[1]) + (sS[2] + sS[3]);
         A = (sA[0] + sA[1]) + (sA[2] + sA[3]);
@@ -642,7 +753,7 @@ int slice_elems(int B, int V, int cus) {
     // long slices once they fill the chip
     const int64_t one = (int64_t)kLpThreads * kLpLong;
     if (V <= kLpThreads * kLpShort) return kLpThreads * kLpShort;
-    if (V <= one || (int64_t)B * ((V + one - 1) / one) >= 8 * cus) return (int)one;
+    if (V <= one || (int64_t)B * ((V + one - 1) / one) >= 2 * cus) return (int)one;
     return kLpThreads * kLpShort;
 }
 
