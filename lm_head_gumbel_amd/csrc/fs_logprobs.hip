@@ -366,6 +366,7 @@ __device__ __forceinline__ void write_best_of(TopShared<E>& s, uint32_t bound, I
         for (int i = t; i < c; i += kLpThreads) {
             const uint64_t key = s.key[i];
             int r = 0;
+#pragma unroll 8
             for (int j = 0; j < c; ++j) r += s.key[j] > key;
             if (r < n) write(r, key);
         }
@@ -601,6 +602,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs 
             for (int i = t; i < slices; i += kLpThreads) {
                 const uint64_t head = list[(size_t)i * n];
                 int r = 0;
+#pragma unroll 8
                 for (int j = 0; j < slices; ++j) r += list[(size_t)j * n] > head;
                 if (r == n - 1 && head) bound = head;   // (keys differ: one thread)
             }
@@ -628,6 +630,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs 
             for (int i = t; i < count; i += kLpThreads) {
                 const uint64_t key = keys[i];
                 int r = 0;
+#pragma unroll 8
                 for (int j = 0; j < count; ++j) r += keys[j] > key;
                 if (r < n) write_best(a, b, r, key, T, m, logS);
             }
