@@ -45,6 +45,7 @@ struct QuantPlan {
     int ksplit;    // waves that share a row block (resident only)
     bool chunked;  // H passes through LDS in chunks (else it stays there whole)
     int G;         // workgroups along V
+    int per_pass;  // 16-row blocks per workgroup and pass
     int grid_y;
     size_t h_bytes, s_bytes;   // LDS: one chunk of H, and of its sums
     size_t pair_off, lds;      // the waves' scales, and all
@@ -88,38 +89,51 @@ __device__ __forceinline__ bf16x8 unpack_word(uint32_t w, uint32_t mask, uint32_
 
 // The same order for 8 bfloat16 of H.
 __device__ __forceinline__ u32x4 permute_h(u32x4 h) {
-    return u32x4{(h.x & 0xFFFFu) | (h.z << 16), (h.x >> 16) | (h.z & 0xFFFF0000u),
-                 (h.y & 0xFFFFu) | (h.w << 16), (h.y >> 16) | (h.w & 0xFFFF0000u)};
+    constexpr uint32_t kLow = 0x05040100u, kHigh = 0x07060302u;   // halves of (second, first)
+    return u32x4{__builtin_amdgcn_perm(h.z, h.x, kLow), __builtin_amdgcn_perm(h.z, h.x, kHigh),
+                 __builtin_amdgcn_perm(h.w, h.y, kLow), __builtin_amdgcn_perm(h.w, h.y, kHigh)};
 }
 
-__device__ __forceinline__ float sum8(u32x4 h) {
-    float s = 0.f;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// s + the sum of 8 bfloat16, in FP32 (products with 1 are exact).
+__device__ __forceinline__ float add8(float s, u32x4 h) {
+    const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        s += __uint_as_float(h[i] << 16) + __uint_as_float(h[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = h[i];
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), one, s, false);
+    }
     return s;
+}
+// The sum of the four lanes l, l + 16, l + 32, l + 48, in all of them.
+__device__ __forceinline__ float add_quarters(float s) {
+    uint32_t u = __float_as_uint(s);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    u = __float_as_uint(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 // Scales and zero points of one block of 128 k of a row, as they lie in
 // memory (NS scales of 2 or 4 bytes, NS bytes).
-template <int NS, int ST>
+template <int NS, int SB>
 struct Groups {
-    static constexpr int kWords = ST == FS_F32 ? NS : (NS + 1) / 2;
+    static constexpr int kWords = SB == 4 ? NS : (NS + 1) / 2;
     uint32_t s[kWords];
     uint32_t z;
 };
-template <int NS, int ST>
-__device__ __forceinline__ float group_scale(const Groups<NS, ST>& g, int n) {
-    if constexpr (ST == FS_F32) return __uint_as_float(g.s[n]);
+template <int NS, int SB>
+__device__ __forceinline__ float group_scale(const Groups<NS, SB>& g, int n, bool bf16) {
+    if constexpr (SB == 4) return __uint_as_float(g.s[n]);
     const uint32_t raw = n % 2 ? g.s[n / 2] >> 16 : g.s[n / 2];
-    return ST == FS_BF16 ? __uint_as_float(raw << 16)
-                         : (float)__builtin_bit_cast(_Float16, (uint16_t)raw);
+    const float f = (float)__builtin_bit_cast(_Float16, (uint16_t)raw);
+    return bf16 ? __uint_as_float(raw << 16) : f;
 }
 // Drops the first sh groups (the same sh for the whole wave).
-template <int NS, int ST>
-__device__ __forceinline__ void end_groups(Groups<NS, ST>& g, int sh) {
+template <int NS, int SB>
+__device__ __forceinline__ void end_groups(Groups<NS, SB>& g, int sh) {
     g.z >>= 8 * sh;
-    if constexpr (ST == FS_F32) {
+    if constexpr (SB == 4) {
         for (; sh > 0; --sh)
 #pragma unroll
             for (int n = 0; n + 1 < NS; ++n) g.s[n] = g.s[n + 1];
@@ -146,13 +160,11 @@ __device__ __forceinline__ void load_bytes(uint32_t* dst, const char* p) {
     }
 }
 
-template <int NB, int MR, int SUB, int ST, bool CHUNKED>
-__global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
-                                                                           QuantPlan pl,
-                                                                           int group_blocks) {
+template <int NB, int MR, int SUB, int SB, bool CHUNKED>
+__device__ __forceinline__ void quant_body(const QuantArgs& a, const QuantPlan& pl,
+                                           int group_blocks) {
     extern __shared__ __align__(16) char smem[];
     constexpr int NS = 4 / SUB;
-    constexpr int SB = ST == FS_F32 ? 4 : 2;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, q = lane >> 4;
@@ -161,16 +173,19 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
     const int nks = a.d / 8;   // pieces of 8 k
     const int nmb = (a.V + 15) / 16;
     const int RW = kQWaves / pl.ksplit, rw = wave / pl.ksplit, kw = wave % pl.ksplit;
-    // pass p of all workgroups sweeps one region of W: blocks p G RW MR ..
-    const int per_pass = RW * MR;
+    // pass p of all workgroups sweeps one region of W, per_pass blocks each
+    const int per_pass = pl.per_pass;
     const int ntile = (nmb + per_pass - 1) / per_pass;
     const int npass = (ntile - (int)blockIdx.x + pl.G - 1) / pl.G;
-    auto pass_begin = [&](int pass) { return ((int)blockIdx.x + pass * pl.G) * per_pass; };
+    auto block_of = [&](int pass, int m) {
+        return ((int)blockIdx.x + pass * pl.G) * per_pass + m * RW + rw;
+    };
 
     // this wave's k blocks of every pass
     const int kper = pl.nkb / pl.ksplit;
     const int kfirst = kw * kper;
     const bool has_zero = a.zero != nullptr;
+    const bool scale_bf16 = a.scale_dtype == FS_BF16;
     const int row_bytes = a.d / 2;
     const char* zp = reinterpret_cast<const char*>(a.zero);
 
@@ -180,7 +195,7 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
     const char* qrow[MR];
     auto row_of = [&](int pass, int m, int r) {
         // rows past V re-read row V - 1 (not stored)
-        return min((pass_begin(pass) + rw * MR + m) * 16 + r, a.V - 1);
+        return min(block_of(pass, m) * 16 + r, a.V - 1);
     };
     auto rows_of = [&](int pass) {
 #pragma unroll
@@ -211,9 +226,9 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
     constexpr int kSlots = pair_slots(NB, NS);
     const int srow = lane >> 2, skb = lane & 3;
     float2* const pairs = reinterpret_cast<float2*>(smem + pl.pair_off) +
-                          wave * (MR * kSlots * NS * 16);
+                          wave * (pl.mr * kSlots * NS * 16);
     int sc_pass = 0, sc_k = 0;
-    Groups<NS, ST> graw[MR];
+    Groups<NS, SB> graw[MR];
     auto load_scales = [&]() __attribute__((always_inline)) {
         const int kb = kfirst + sc_k + skb;
         // where the row ends inside the block, the row's last NS groups
@@ -238,7 +253,7 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
 #pragma unroll
             for (int n = 0; n < NS; ++n)
                 pairs[((m * kSlots + slot) * NS + n) * 16 + srow] =
-                    make_float2(group_scale(graw[m], n),
+                    make_float2(group_scale(graw[m], n, scale_bf16),
                                 -16.f - (float)((graw[m].z >> (8 * n)) & 0xFFu));
         }
         }
@@ -265,10 +280,8 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
     auto store_unit = [&](char* buf, int u, const u32x4 (&h)[4]) {
         const int kb = u / NB, col = (u % NB) * 16 + r16;
         float* hs = reinterpret_cast<float*>(buf + pl.h_bytes);
-        float part[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            part[i] = sum8(h[i]);
             // piece i * 4 + q: its step and quarter
             const int step = SUB == 4 ? q : SUB == 1 ? i : (i >> 1) * 2 + (q & 1);
             const int qq = SUB == 4 ? i : SUB == 1 ? q : (i & 1) + (q >> 1) * 2;
@@ -280,9 +293,8 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
         for (int n = 0; n < NS; ++n) {
             float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < SUB; ++i) s += part[n * SUB + i];
-            s += __shfl_xor(s, 16, 64);
-            s += __shfl_xor(s, 32, 64);
+            for (int i = 0; i < SUB; ++i) s = add8(s, h[n * SUB + i]);
+            s = add_quarters(s);
             if (q == 0) hs[(kb * NS + n) * (16 * NB) + col] = s;
         }
     };
@@ -306,18 +318,6 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
         uint32_t frag = buf + frag0 + kb_lds * 4 * frag_step;
         uint32_t sums = buf + sums0 + kb_lds * (64 * NB * NS);
         asm volatile("" : "+v"(frag), "+v"(sums));   // one address each, formed here
-        // operands of H: all four steps read ahead for one column block, else
-        // one step ahead
-        constexpr int kAhead = NB == 1 ? 4 : 2;
-        bf16x8 hf[kAhead][NB];
-        auto read_h = [&](int j) __attribute__((always_inline)) {
-#pragma unroll
-            for (int c = 0; c < NB; ++c)
-                hf[j % kAhead][c] =
-                    *reinterpret_cast<const bf16x8*>(smem + frag + j * frag_step + c * 256);
-        };
-#pragma unroll
-        for (int j = 0; j < kAhead - (NB == 1 ? 0 : 1); ++j) read_h(j);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             f32x4 acc[MR][NB];
@@ -337,17 +337,18 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
 #pragma unroll
             for (int jj = 0; jj < SUB; ++jj) {
                 const int j = n * SUB + jj;
-                if (NB > 1 && j + 1 < 4) read_h(j + 1);
                 bf16x8 wf[MR];
 #pragma unroll
                 for (int m = 0; m < MR; ++m) wf[m] = unpack_word(wt[m][j], nib_mask, sixteen);
 #pragma unroll
-                for (int c = 0; c < NB; ++c)
+                for (int c = 0; c < NB; ++c) {
+                    const bf16x8 hf =
+                        *reinterpret_cast<const bf16x8*>(smem + frag + j * frag_step + c * 256);
 #pragma unroll
                     for (int m = 0; m < MR; ++m)
-                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            hf[j % kAhead][c], wf[m], acc[m][c], 0, 0, 0);
-                if (NB > 1) __builtin_amdgcn_sched_barrier(0);
+                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf, wf[m], acc[m][c], 0,
+                                                                            0, 0);
+                }
             }
 #pragma unroll
             for (int m = 0; m < MR; ++m)
@@ -359,7 +360,14 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
                         // here, not after the next loads (acc would stay alive)
                         asm volatile("" : "+v"(total[m][c][i]));
                     }
-            if constexpr (NS > 1) __builtin_amdgcn_sched_barrier(0);   // one group at a time
+        }
+        // matrix and vector instructions in turn: each matrix instruction
+        // occupies its unit for the issue of three vector ones
+        constexpr int kPer = 8 / NB + 2 * NS + 1;
+#pragma unroll
+        for (int i = 0; i < 4 * NB * MR; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, kPer, 0);
         }
     };
     // kQDepth blocks of k, from block k of the chunk at `buf`
@@ -376,7 +384,9 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
                 __builtin_amdgcn_sched_barrier(0);
             }
             consume(buf, k + i, i % kSlots, w[i]);
+            __builtin_amdgcn_sched_barrier(0);
             consume(buf, k + i + 1, i % kSlots + 1, w[i + 1]);
+            __builtin_amdgcn_sched_barrier(0);
             load(w[i], w[i + 1]);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -388,11 +398,10 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
             for (int c = 0; c < NB; ++c) total[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
     auto store = [&](int pass) {
-        const int s = pass_begin(pass) + rw * MR;
 #pragma unroll
         for (int m = 0; m < MR; ++m) {
-            const int row = (s + m) * 16 + r16;
-            if (row >= a.V) continue;
+            const int row = block_of(pass, m) * 16 + r16;
+            if (m * RW + rw >= per_pass || row >= a.V) continue;
 #pragma unroll
             for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -441,7 +450,7 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
                 const float* at = sums + ((t * kQWaves + rw * pl.ksplit) * 64 + lane) * 4 + i;
                 float sum = at[0];
                 for (int o = 1; o < pl.ksplit; ++o) sum += at[o * 256];
-                const int row = (pass_begin(pass) + rw * MR + t / NB) * 16 + r16;
+                const int row = block_of(pass, t / NB) * 16 + r16;
                 const int b = col0 + t % NB * 16 + q * 4 + i;
                 if (row < a.V && b < a.B) a.logits[(size_t)b * a.V + row] = sum;
             }
@@ -471,6 +480,20 @@ __global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a,
             store(pass);
         }
     }
+}
+
+template <int NB, int MR, int SUB, int SB, bool CHUNKED>
+__global__ __launch_bounds__(kQThreads, 2) void quant_kernel(QuantArgs a, QuantPlan pl,
+                                                             int group_blocks) {
+    if constexpr (CHUNKED && MR > 1) {
+        // the last waves of a pass may have fewer blocks
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        if ((MR - 1) * kQWaves + wave >= pl.per_pass) {
+            quant_body<NB, MR - 1, SUB, SB, CHUNKED>(a, pl, group_blocks);
+            return;
+        }
+    }
+    quant_body<NB, MR, SUB, SB, CHUNKED>(a, pl, group_blocks);
 }
 
 constexpr size_t kQLds = 160 * 1024;
@@ -509,7 +532,8 @@ QuantPlan quant_plan(const QuantArgs& a, int cus) {
         p.lds = bytes(p.KC) + rest(p.mr);
         int occ = (int)(kQLds / p.lds);
         if (occ > 2) occ = 2;
-        const int ntile = (nmb + (kQWaves / p.ksplit) * p.mr - 1) / ((kQWaves / p.ksplit) * p.mr);
+        p.per_pass = (kQWaves / p.ksplit) * p.mr;
+        const int ntile = (nmb + p.per_pass - 1) / p.per_pass;
         p.G = ntile < cus * occ ? ntile : cus * occ;
     } else {
         if (p.nb == 1) p.nb = 2;   // (chunks are built for two column blocks or four)
@@ -521,37 +545,41 @@ QuantPlan quant_plan(const QuantArgs& a, int cus) {
         p.nchunks = p.nkb / p.KC;
         p.pair_off = (p.nchunks == 1 ? 1 : 2) * bytes(p.KC);
         p.lds = p.pair_off + rest(p.mr);   // at most 152 KiB (group 32)
-        const int ntile = (nmb + kQWaves * p.mr - 1) / (kQWaves * p.mr);
-        p.G = ntile < cus ? ntile : cus;
+        // as many passes as full ones take, of equal length
+        const int full = kQWaves * p.mr;
+        p.G = nmb < cus ? nmb : cus;
+        const int npass = (nmb + p.G * full - 1) / (p.G * full);
+        p.per_pass = (nmb + p.G * npass - 1) / (p.G * npass);
+        const int ntile = (nmb + p.per_pass - 1) / p.per_pass;
+        if (p.G > ntile) p.G = ntile;
     }
     p.grid_y = (a.B + 16 * p.nb - 1) / (16 * p.nb);
     return p;
 }
 
-template <int NB, int MR, int SUB, int ST, bool CHUNKED>
+template <int NB, int MR, int SUB, int SB, bool CHUNKED>
 hipError_t launch(const QuantArgs& a, const QuantPlan& p, hipStream_t stream) {
     const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&quant_kernel<NB, MR, SUB, ST, CHUNKED>),
+        hipFuncSetAttribute(reinterpret_cast<const void*>(&quant_kernel<NB, MR, SUB, SB, CHUNKED>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)kQLds);
     if (e != hipSuccess) return e;
     const int group_blocks = a.group >= kQBlock ? a.group / kQBlock : 1;
-    hipLaunchKernelGGL((quant_kernel<NB, MR, SUB, ST, CHUNKED>), dim3(p.G, p.grid_y), dim3(kQThreads),
-                       p.lds, stream, a, p, group_blocks);
+    hipLaunchKernelGGL((quant_kernel<NB, MR, SUB, SB, CHUNKED>), dim3(p.G, p.grid_y),
+                       dim3(kQThreads), p.lds, stream, a, p, group_blocks);
     return hipGetLastError();
 }
 
-template <int NB, int MR, int ST, bool CHUNKED>
+template <int NB, int MR, int SB, bool CHUNKED>
 hipError_t launch_sub(const QuantArgs& a, const QuantPlan& p, hipStream_t stream) {
-    return a.group == 32   ? launch<NB, MR, 1, ST, CHUNKED>(a, p, stream)
-           : a.group == 64 ? launch<NB, MR, 2, ST, CHUNKED>(a, p, stream)
-                           : launch<NB, MR, 4, ST, CHUNKED>(a, p, stream);
+    return a.group == 32   ? launch<NB, MR, 1, SB, CHUNKED>(a, p, stream)
+           : a.group == 64 ? launch<NB, MR, 2, SB, CHUNKED>(a, p, stream)
+                           : launch<NB, MR, 4, SB, CHUNKED>(a, p, stream);
 }
 
 template <int NB, int MR, bool CHUNKED>
 hipError_t launch_nb(const QuantArgs& a, const QuantPlan& p, hipStream_t stream) {
-    return a.scale_dtype == FS_F32    ? launch_sub<NB, MR, FS_F32, CHUNKED>(a, p, stream)
-           : a.scale_dtype == FS_BF16 ? launch_sub<NB, MR, FS_BF16, CHUNKED>(a, p, stream)
-                                      : launch_sub<NB, MR, FS_F16, CHUNKED>(a, p, stream);
+    return a.scale_dtype == FS_F32 ? launch_sub<NB, MR, 4, CHUNKED>(a, p, stream)
+                                   : launch_sub<NB, MR, 2, CHUNKED>(a, p, stream);
 }
 
 // d below one block of 128: one thread per logit, w = s (q - z) in FP32.
