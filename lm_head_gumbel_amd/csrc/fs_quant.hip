@@ -310,64 +310,94 @@ __device__ __forceinline__ void quant_body(const QuantArgs& a, const QuantPlan& 
     // and-or)
     uint32_t nib_mask = 0x00780078u, sixteen = 0x41804180u;
     asm volatile("" : "+s"(nib_mask), "+v"(sixteen));
-    auto consume = [&](int buf, int kb_lds, int slot,
-                       const u32x4 (&wv)[MR]) __attribute__((always_inline)) {
-        u32x4 wt[MR];
+    // Two blocks of k: eight matrix steps, their LDS operands read kAheadH steps
+    // before use, matrix and vector instructions in turn.
+    auto consume = [&](int buf, int kb_lds, int slot, const u32x4 (&w0)[MR],
+                       const u32x4 (&w1)[MR]) __attribute__((always_inline)) {
+        constexpr int kSteps = 8;
+        constexpr int kAheadH = NB == 1 ? 3 : NB == 2 ? 2 : 1;   // a step's latency to hide
+        constexpr int kBufs = kAheadH + 1;
+        u32x4 wt[2][MR];
 #pragma unroll
-        for (int m = 0; m < MR; ++m) wt[m] = transpose_words<SUB>(wv[m]);
+        for (int m = 0; m < MR; ++m) {
+            wt[0][m] = transpose_words<SUB>(w0[m]);
+            wt[1][m] = transpose_words<SUB>(w1[m]);
+        }
         uint32_t frag = buf + frag0 + kb_lds * 4 * frag_step;
         uint32_t sums = buf + sums0 + kb_lds * (64 * NB * NS);
         asm volatile("" : "+v"(frag), "+v"(sums));   // one address each, formed here
+        bf16x8 hf[kBufs][NB];
+        f32x4 hsum[2][NB];
+        float2 sc[2][MR];
+        auto group_of = [](int st) { return st / SUB; };
+        auto read = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            f32x4 acc[MR][NB];
-            float s[MR], off[MR];
+            for (int c = 0; c < NB; ++c)
+                hf[st % kBufs][c] =
+                    *reinterpret_cast<const bf16x8*>(smem + frag + st * frag_step + c * 256);
+            if (st % SUB == 0) {
+                const int g = group_of(st);
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                const float2 v = pairs[((m * kSlots + slot) * NS + n) * 16 + r16];
-                s[m] = v.x;
-                off[m] = v.y;
+                for (int c = 0; c < NB; ++c)
+                    hsum[g % 2][c] =
+                        *reinterpret_cast<const f32x4*>(smem + sums + (g * NB + c) * 64);
+#pragma unroll
+                for (int m = 0; m < MR; ++m)
+                    sc[g % 2][m] =
+                        pairs[((m * kSlots + slot + g / NS) * NS + g % NS) * 16 + r16];
             }
+        };
+        // (hsum and sc hold two groups, the one in use and the next)
+        constexpr int kAhead = kAheadH < SUB ? kAheadH : SUB;
 #pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                const f32x4 h = *reinterpret_cast<const f32x4*>(smem + sums + (n * NB + c) * 64);
+        for (int st = 0; st < kAhead; ++st) read(st);
+        f32x4 acc[MR][NB];
 #pragma unroll
-                for (int m = 0; m < MR; ++m) acc[m][c] = h * off[m];
-            }
-#pragma unroll
-            for (int jj = 0; jj < SUB; ++jj) {
-                const int j = n * SUB + jj;
-                bf16x8 wf[MR];
-#pragma unroll
-                for (int m = 0; m < MR; ++m) wf[m] = unpack_word(wt[m][j], nib_mask, sixteen);
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                    const bf16x8 hf =
-                        *reinterpret_cast<const bf16x8*>(smem + frag + j * frag_step + c * 256);
-#pragma unroll
-                    for (int m = 0; m < MR; ++m)
-                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf, wf[m], acc[m][c], 0,
-                                                                            0, 0);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < MR; ++m)
+        for (int st = 0; st < kSteps; ++st) {
+            if (st + kAhead < kSteps) read(st + kAhead);
+            const int g = group_of(st);
+            if (st % SUB == 0)
 #pragma unroll
                 for (int c = 0; c < NB; ++c)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        total[m][c][i] = fmaf(s[m], acc[m][c][i], total[m][c][i]);
-                        // here, not after the next loads (acc would stay alive)
-                        asm volatile("" : "+v"(total[m][c][i]));
-                    }
-        }
-        // matrix and vector instructions in turn: each matrix instruction
-        // occupies its unit for the issue of three vector ones
-        constexpr int kPer = 8 / NB + 2 * NS + 1;
+                    for (int m = 0; m < MR; ++m) acc[m][c] = hsum[g % 2][c] * sc[g % 2][m].y;
+            bf16x8 wf[MR];
 #pragma unroll
-        for (int i = 0; i < 4 * NB * MR; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, kPer, 0);
+            for (int m = 0; m < MR; ++m)
+                wf[m] = unpack_word(wt[st / 4][m][st % 4], nib_mask, sixteen);
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+#pragma unroll
+                for (int m = 0; m < MR; ++m)
+                    acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf[st % kBufs][c], wf[m],
+                                                                        acc[m][c], 0, 0, 0);
+            if (st % SUB == SUB - 1)
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+#pragma unroll
+                    for (int m = 0; m < MR; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            total[m][c][i] = fmaf(sc[g % 2][m].x, acc[m][c][i], total[m][c][i]);
+                            // here, not after the next loads (acc would stay alive)
+                            asm volatile("" : "+v"(total[m][c][i]));
+                        }
+        }
+        constexpr int kPer = 8 / NB + 2 * NS + 1;   // vector instructions per matrix one
+#pragma unroll
+        for (int st = -kAhead; st < kSteps; ++st) {
+            if (st + kAhead < kSteps) {
+                if ((st + kAhead) % SUB == 0)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2 * NB + (MR + 1) / 2, 0);
+                else
+                    __builtin_amdgcn_sched_group_barrier(0x100, NB, 0);
+            }
+            if (st < 0) continue;
+#pragma unroll
+            for (int i = 0; i < NB * MR; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, kPer, 0);
+            }
         }
     };
     // kQDepth blocks of k, from block k of the chunk at `buf`
@@ -383,9 +413,7 @@ __device__ __forceinline__ void quant_body(const QuantArgs& a, const QuantPlan& 
                 __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
                 __builtin_amdgcn_sched_barrier(0);
             }
-            consume(buf, k + i, i % kSlots, w[i]);
-            __builtin_amdgcn_sched_barrier(0);
-            consume(buf, k + i + 1, i % kSlots + 1, w[i + 1]);
+            consume(buf, k + i, i % kSlots, w[i], w[i + 1]);
             __builtin_amdgcn_sched_barrier(0);
             load(w[i], w[i + 1]);
             __builtin_amdgcn_sched_barrier(0);

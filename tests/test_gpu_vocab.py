@@ -67,7 +67,9 @@ def quant_bound(Hf, q, Sf, z, group):
     (64, 384, 77, 128, "f16", False), (65, 128, 200, 64, "bf16", True), (130, 512, 96, 512, "f32", True),
     (1, 4096, 2000, 128, "bf16", True), (20, 5120, 300, 128, "f16", False), (48, 2048, 515, 64, "bf16", True),
     (7, 4096, 515, 32, "f32", True), (64, 2080, 300, 32, "bf16", False), (300, 160, 60, 32, "f16", True),
-    (16, 8192, 600, 128, "bf16", True), (24, 8192, 200, 32, "f32", True), (18, 6144, 200, 64, "f16", True)])
+    (16, 8192, 600, 128, "bf16", True), (24, 8192, 200, 32, "f32", True), (18, 6144, 200, 64, "f16", True),
+    (5, 1024, 300, 64, "bf16", True), (12, 1152, 100, 32, "f16", True), (2, 2048, 9000, 64, "f32", False),
+    (30, 1024, 9000, 32, "bf16", True), (64, 1024, 9000, 128, "f32", True), (50, 640, 20000, 64, "bf16", True)])
 def test_quant_logits_match_the_oracle(B, d, V, group, sdt, zero):
     H, Hf, q, S, Sf, z = quant_problem(B, d, V, group, sdt, zero, seed=B + d)
     t = torch()
