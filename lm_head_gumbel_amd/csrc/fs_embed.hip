@@ -39,15 +39,23 @@ __device__ __forceinline__ void load_row(const typename Elem<DT>::type* row, int
         for (int e = 0; e < N; ++e) x[e] = k + e < d ? (float)row[k + e] : 0.f;
     }
 }
-// N values to elements k .. of a row of d.
-template <int DT, int N>
+// N values to elements k .. of a row of d; STREAM: past the caches, for what
+// is not read again soon.
+template <int DT, int N, bool STREAM = false>
 __device__ __forceinline__ void store_row(typename Elem<DT>::type* row, int k, int d,
                                           const float* x) {
     typename Elem<DT>::type v[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) v[e] = (typename Elem<DT>::type)x[e];
     if (k + N <= d) {
-        __builtin_memcpy(row + k, v, sizeof(v));
+        if constexpr (STREAM && sizeof(v) == 16) {
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+            u32x4 w;
+            __builtin_memcpy(&w, v, 16);
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(row + k));
+        } else {
+            __builtin_memcpy(row + k, v, sizeof(v));
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < N; ++e)
@@ -83,7 +91,7 @@ __global__ __launch_bounds__(kEmThreads) void embed_kernel(EmbedArgs a, int lane
                 // (a row outside the shard is 0, also with an infinite scale)
 #pragma unroll
                 for (int e = 0; e < N; ++e) x[u][e] = in ? a.scale * x[u][e] : 0.f;
-                if (ku < a.d) store_row<DT, N>(out, ku, a.d, x[u]);
+                if (ku < a.d) store_row<DT, N, true>(out, ku, a.d, x[u]);
             }
         }
     }
@@ -173,27 +181,37 @@ __device__ __forceinline__ void scan_digits(SortShared& s, uint32_t v) {
     __syncthreads();
 }
 
-// Few tokens: each finds its place by counting the keys before it.
+// Few tokens: each finds its place by counting the keys before it, four
+// threads a token (a quarter of the keys each).
 constexpr int kFew = 1024;
+constexpr int kFewPer = kEmThreads / 4;   // tokens per workgroup
 __global__ __launch_bounds__(kEmThreads) void sort_few_kernel(const int32_t* ids, int N,
                                                               int v_offset, int V,
                                                               uint32_t* out_key,
                                                               uint32_t* out_pos) {
     __shared__ __align__(16) uint32_t key[kFew];
-    for (int i = threadIdx.x; i < kFew; i += kEmThreads)
-        key[i] = i < N ? row_key_of(ids[i], v_offset, V) : ~0u;
+#pragma unroll
+    for (int i = 0; i < kFew / kEmThreads; ++i) {
+        const int j = i * kEmThreads + threadIdx.x;
+        key[j] = j < N ? row_key_of(ids[j], v_offset, V) : ~0u;
+    }
     __syncthreads();
-    const int n = blockIdx.x * kEmThreads + threadIdx.x;
-    if (n >= N) return;
+    const int n = min((int)(blockIdx.x * kFewPer + threadIdx.x / 4), N - 1);
+    const int part = threadIdx.x % 4;
     const uint32_t mine = key[n];
     int at = 0;
-    for (int i = 0; i < N; i += 4) {
+#pragma unroll 4
+    for (int i = part * 4; i < N; i += 16) {
         const uint4 k = *reinterpret_cast<const uint4*>(key + i);
         at += (k.x < mine || (k.x == mine && i < n)) + (k.y < mine || (k.y == mine && i + 1 < n)) +
               (k.z < mine || (k.z == mine && i + 2 < n)) + (k.w < mine || (k.w == mine && i + 3 < n));
     }
-    out_key[at] = mine;
-    out_pos[at] = n;
+    at += __shfl_xor(at, 1, 64);
+    at += __shfl_xor(at, 2, 64);
+    if (part == 0 && blockIdx.x * kFewPer + threadIdx.x / 4 < N) {
+        out_key[at] = mine;
+        out_pos[at] = n;
+    }
 }
 
 // One tile: the whole sort in LDS.
@@ -380,7 +398,7 @@ __device__ void zero_rows(const SumArgs& a, uint32_t row0) {
         if (row >= (uint32_t)a.V || ((named[r / 32] >> (r % 32)) & 1u)) continue;
         O* out = static_cast<O*>(a.dW) + (size_t)row * a.d;
         for (int k = t % a.zero_lanes * N; k < a.d; k += a.zero_lanes * N)
-            store_row<DO, N>(out, k, a.d, zero);
+            store_row<DO, N, true>(out, k, a.d, zero);
     }
     __syncthreads();   // before the next rows' marks
 }
@@ -579,8 +597,8 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, void* ws, hipStream_t strea
     while (passes * kDigitBits < 32 && ((uint32_t)a.V >> (passes * kDigitBits)) != 0) ++passes;
     int at = 0;   // the arrays that hold the sorted tokens
     if (a.N > 0 && a.N <= kFew) {
-        hipLaunchKernelGGL(sort_few_kernel, dim3((a.N + kEmThreads - 1) / kEmThreads), dim3(kEmThreads), 0,
-                           stream, a.ids, a.N, a.v_offset, a.V, u32(lay.key[0]), u32(lay.pos[0]));
+        hipLaunchKernelGGL(sort_few_kernel, dim3((a.N + kFewPer - 1) / kFewPer),
+                           dim3(kEmThreads), 0, stream, a.ids, a.N, a.v_offset, a.V, u32(lay.key[0]), u32(lay.pos[0]));
     } else if (a.N > 0 && a.N <= kTile) {
         hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSortThreads), 0, stream, a.ids, a.N,
                            a.v_offset, a.V, passes, u32(lay.key[0]), u32(lay.pos[0]));
