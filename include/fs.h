@@ -279,9 +279,9 @@ typedef struct {
  * w[j, k] (FP32 sums, no temperature, no mask) to device logits [B, V]
  * row-major, ready for fs_multinomial and fs_logprobs.  Each group's sum of
  * H q is formed first, in FP32, and scaled once, so the weights are never
- * rounded to bfloat16.  H as defined above (finite values: an infinite or NaN
- * H[b, k] makes row b NaN).  B, d, V of p are read; d must be a multiple of
- * the group.  No workspace. */
+ * rounded to bfloat16.  H as defined above; an infinite or NaN H[b, k] leaves
+ * row b without finite values.  B, d, V of p are read; d must be a multiple of
+ * the group.  V above 2^31 - 2^20 - 1 is FS_ERR_UNSUPPORTED.  No workspace. */
 fs_status fs_logits_quant(const fs_params* p, const void* H, const fs_quant* W, float* logits,
                           void* stream);
 

@@ -50,9 +50,10 @@ def quant(q, scale, zero, group, scale_dtype=None):
     """Build an fs_quant from q [V, d / 2] uint8, scale [V, d / group] and zero
     (uint8 [V, d / group] or None): tensors, which it keeps alive, or raw
     addresses (then scale_dtype must be given)."""
-    at = _operands((q, scale, zero))
+    at = _operands((q, scale, zero), "u*u")
     if at is None:
-        raise ValueError("quant: tensors must be contiguous and on the current device")
+        raise ValueError("quant: tensors must be contiguous, on the current device, and q and "
+                         "zero uint8")
     w = fs_quant(*at, group, _dtype(scale, scale_dtype))
     w.tensors = (q, scale, zero)
     return w
@@ -169,15 +170,29 @@ def _device():
     return _torch._C._cuda_getDevice()
 
 
-def _operands(xs):
+_KINDS = {}
+
+
+def _kinds(kinds):
+    """The element types that _operands' letters name (None: not looked at)."""
+    if _torch is None:
+        return (None,) * len(kinds)
+    types = dict(f=_torch.float32, h=_torch.bfloat16, i=_torch.int32, u=_torch.uint8)
+    return _KINDS.setdefault(kinds, tuple(types.get(k) for k in kinds))
+
+
+def _operands(xs, kinds):
     """The addresses of xs (tensors, raw addresses or None); None if a tensor
-    is not contiguous or not on the current device."""
+    is not contiguous, not on the current device or not of its kind: f float32,
+    h bfloat16, i int32 (or uint32), u uint8, * looked at by the caller or any."""
     dev = _device()
     out = []
-    for x in xs:
+    for x, kind in zip(xs, _KINDS.get(kinds) or _kinds(kinds)):
         if x is None or x.__class__ is int:
             out.append(x)
-        elif x.get_device() != dev or not x.is_contiguous():
+        elif x.get_device() != dev or not x.is_contiguous() or (
+                kind is not None and x.dtype is not kind
+                and not (kind is _torch.int32 and x.dtype is _torch.uint32)):
             return None
         else:
             out.append(x.data_ptr())
@@ -314,7 +329,7 @@ def fs_multinomial(p, logits, temp, allow, out_idx, ws=None, ws_bytes=None, stre
 # device than the current one is FS_ERR_INVALID_ARG.
 
 def fs_logits_quant(p, H, W, logits, stream=None):
-    at = _operands((H, logits))
+    at = _operands((H, logits), "hf")
     if at is None:
         return FS_ERR_INVALID_ARG
     return lib().fs_logits_quant(ctypes.byref(p), at[0], None if W is None else ctypes.byref(W),
@@ -325,7 +340,7 @@ def fs_logprobs(p, logits, temp, allow, token, n_top, out_logprob=None, out_rank
                 out_lse=None, out_entropy=None, top_idx=None, top_logprob=None, ws=None,
                 ws_bytes=None, stream=None, dtype=None, ld=None):
     at = _operands((temp, allow, token, out_logprob, out_rank, out_lse, out_entropy, top_idx,
-                    top_logprob, ws))
+                    top_logprob, ws), "fiififfif*")
     if at is None:
         return FS_ERR_INVALID_ARG
     rows, ld = _rows(logits, p, ld)
@@ -336,7 +351,8 @@ def fs_logprobs(p, logits, temp, allow, token, n_top, out_logprob=None, out_rank
 
 def fs_logprobs_grad(p, logits, temp, allow, token, n_top, top_idx, lse, entropy, g_logprob, g_lse,
                      g_entropy, g_top, grad, stream=None, dtype=None, ld=None, ld_grad=None):
-    at = _operands((temp, allow, token, top_idx, lse, entropy, g_logprob, g_lse, g_entropy, g_top))
+    at = _operands((temp, allow, token, top_idx, lse, entropy, g_logprob, g_lse, g_entropy, g_top),
+                   "fiiiffffff")
     dt = _dtype(logits, dtype)
     if at is None or _dtype(grad, dtype) != dt:
         return FS_ERR_INVALID_ARG
@@ -347,7 +363,7 @@ def fs_logprobs_grad(p, logits, temp, allow, token, n_top, top_idx, lse, entropy
 
 
 def fs_embed(p, ids, W, scale, out, stream=None, dtype=None):
-    at = _operands((ids, W, out))
+    at = _operands((ids, W, out), "i**")
     dt = _dtype(W, dtype)
     if at is None or _dtype(out, dtype) != dt:
         return FS_ERR_INVALID_ARG
@@ -356,7 +372,7 @@ def fs_embed(p, ids, W, scale, out, stream=None, dtype=None):
 
 def fs_embed_grad(p, ids, g, scale, accumulate, dW, ws=None, ws_bytes=None, stream=None,
                   dtype=None, dw_dtype=None):
-    at = _operands((ids, g, dW, ws))
+    at = _operands((ids, g, dW, ws), "i***")
     if at is None:
         return FS_ERR_INVALID_ARG
     return lib().fs_embed_grad(ctypes.byref(p), at[0], at[1], _dtype(g, dtype), scale, accumulate,

@@ -467,6 +467,7 @@ fs_status fs_logits_quant(const fs_params* p, const void* H, const fs_quant* W, 
     if (!W || elem_size(W->scale_dtype) == 0 || W->group < 1) return FS_ERR_INVALID_ARG;
     if (p->B == 0 || p->V == 0) return FS_OK;
     if (!logits) return FS_ERR_INVALID_ARG;
+    if (p->V > kMaxQuantRow) return FS_ERR_UNSUPPORTED;
     if (W->group != 32 && W->group != 64 && W->group % 128 != 0) return FS_ERR_UNSUPPORTED;
     if (p->d % W->group != 0) return FS_ERR_UNSUPPORTED;
     if (p->d > 0 && !W->scale) return FS_ERR_INVALID_ARG;

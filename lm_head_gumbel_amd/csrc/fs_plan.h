@@ -165,6 +165,9 @@ constexpr int kMaxAlternatives = 64;   // n_top of fs_logprobs
 // Ids of a row of fs_logprobs and its gradient: ids past the last, up to the
 // end of the last slice, still fit an int.
 constexpr int kMaxRow = INT32_MAX - 65536;
+// Rows of W of fs_logits_quant: the rows of its last pass still fit an int
+// (cus * 2 workgroups of 16 blocks of 16 rows).
+constexpr int kMaxQuantRow = INT32_MAX - (1 << 20);
 // Plan of a call that passed check_params with B > 0 and V > 0, on a device
 // with `cus` compute units.  variant: Stage1Variant.
 void make_plan(const fs_params* p, int variant, int cus, Plan& pl);

@@ -548,6 +548,11 @@ def test_embed_gradient_matches_the_oracle(N, d, V, kind, dtype, out):
     assert np.array_equal(f64(acc)[count[:, 0] == 0], basef[count[:, 0] == 0])
 
 
+@pytest.mark.parametrize("kind,dtype,out", [("zipf", "bf16", "bf16"), ("two", "f32", "f32"), ("any", "f16", "f32")])
+def test_embed_gradient_of_long_lists(kind, dtype, out):
+    test_embed_gradient_matches_the_oracle(17000, 1001, 300, kind, dtype, out)   # (chunks of 32)
+
+
 def test_embed_gradient_is_the_same_every_time():
     t = torch()
     rng = np.random.default_rng(2)
@@ -603,6 +608,66 @@ def test_tensors_that_do_not_fit_are_refused():
     assert fs.fs_embed(p, ids, z(4, 8), 1.0, t.zeros(2, 8)) == BAD
     assert fs.fs_embed_grad(p, ids, z(8, 2).T, 1.0, 0, z(4, 8), z(1 << 16, dtype=t.uint8)) == BAD
     t.cuda.synchronize()
+
+
+def test_tensors_of_another_type_are_refused():
+    t = torch()
+    z = lambda *s, **k: t.zeros(s, device="cuda", **k)  # noqa: E731
+    p, BAD = fs.params(2, 64, 4), fs.FS_ERR_INVALID_ARG
+    ids, long = z(2, dtype=t.int32), z(2, dtype=t.int64)
+    ws = z(1 << 16, dtype=t.uint8)
+    l, row = z(2, 4), z(2)
+    idx, val = z(2, 1, dtype=t.int32), z(2, 1)
+    call = lambda temp=None, allow=None, tok=ids, lp=row, rank=None, idx=idx, val=val: fs.fs_logprobs(  # noqa: E731
+        p, l, temp, allow, tok, 1, lp, rank, None, None, idx, val, ws)
+    assert call() == call(temp=row, allow=z(2, 1, dtype=t.int32), rank=ids) == fs.FS_OK
+    for bad in (dict(temp=row.double()), dict(allow=z(2, 1, dtype=t.int64)), dict(tok=long), dict(lp=row.half()),
+                dict(rank=long), dict(idx=idx.long()), dict(val=val.double())):
+        assert call(**bad) == BAD, bad
+    grad = lambda lse=row, tok=ids, g=row: fs.fs_logprobs_grad(  # noqa: E731
+        p, l, None, None, tok, 0, None, lse, None, g, None, None, None, z(2, 4))
+    assert grad() == fs.FS_OK
+    assert grad(lse=row.double()) == grad(tok=long) == grad(g=row.bfloat16()) == BAD
+    W, out = z(4, 64), z(2, 64)
+    assert fs.fs_embed(p, ids, W, 1.0, out) == fs.FS_OK
+    assert fs.fs_embed(p, long, W, 1.0, out) == BAD
+    assert fs.fs_embed_grad(p, ids, out, 1.0, 0, W, ws) == fs.FS_OK
+    assert fs.fs_embed_grad(p, long, out, 1.0, 0, W, ws) == BAD
+    q, s = z(4, 32, dtype=t.uint8), z(4, 2, dtype=t.bfloat16)
+    H = z(2, 64, dtype=t.bfloat16)
+    assert fs.fs_logits_quant(p, H, fs.quant(q, s, None, 32), l) == fs.FS_OK
+    assert fs.fs_logits_quant(p, H.half(), fs.quant(q, s, None, 32), l) == BAD
+    assert fs.fs_logits_quant(p, H, fs.quant(q, s, None, 32), l.bfloat16()) == BAD
+    for args in ((q.int(), s, None), (q, s, s)):
+        with pytest.raises(ValueError):
+            fs.quant(*args, 32)
+    t.cuda.synchronize()
+
+
+def test_more_rows_than_a_grid_has():
+    # each workgroup takes a second row: rows repeat with a period of 997
+    t = torch()
+    B, V, per = 66001, 70, 997
+    x = Lp(per, V, "f32", 3, seed=5)
+    g = grads(x, np.random.default_rng(6), ("lp", "lse", "ent", "top"))
+    want, mag = want_grad(x, g)
+    at = t.arange(B, device="cuda") % per
+    big = lambda v: v.index_select(0, at) if hasattr(v, "shape") else v  # noqa: E731
+    p, ws = fs.params(B, 0, V), garbage(fs.fs_workspace_bytes(fs.params(B, 0, V), fs.FS_VARIANT_LOGPROBS, 3))
+    o = {k: big(v) for k, v in x.out().items()}
+    logits, token = big(x.logits), big(x.token)
+    fs.check(fs.fs_logprobs(p, logits, None, None, token, 3, o["logprob"], o["rank"], o["lse"], o["entropy"], o["top_idx"],
+                            o["top_logprob"], ws))
+    out = t.empty_like(logits)
+    d = {k: big(dev(v)) for k, v in g.items()}
+    fs.check(fs.fs_logprobs_grad(p, logits, None, None, token, 3, big(dev(x.want["top_idx"].astype(np.int32))),
+                                 big(dev(x.want["lse"].astype(np.float32))), big(dev(x.want["entropy"].astype(np.float32))),
+                                 d["lp"], d["lse"], d["ent"], d["top"], out))
+    t.cuda.synchronize()
+    x.check({k: v[:per] for k, v in o.items()})
+    check_grad(out[:per], want, mag, "f32")
+    for v in (*o.values(), out):
+        assert bool((v == big(v[:per])).all())
 
 
 def decode_state(seed):

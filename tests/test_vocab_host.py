@@ -103,6 +103,14 @@ def test_quant_refusals():
     assert call(fs.params(2, 64, 0), None, quant(None, None), None) == fs.FS_OK
 
 
+@built
+def test_quant_row_limit():
+    # ids of the last pass have to fit an int
+    over = fs.params(1, 128, 2 ** 31 - 2 ** 20)
+    assert fs.fs_logits_quant(over, 16, quant(), 16) == UNSUP
+    assert fs.fs_logits_quant(over, 16, quant(group=96), None) == BAD
+
+
 def lp(p, logits=16, token=16, n_top=0, logprob=16, idx=None, val=None, dtype=fs.FS_F32, ld=None, **kw):
     return fs.fs_logprobs(p, logits, None, None, token, n_top, logprob, None, None, None, idx, val, 256, 1 << 30,
                           dtype=dtype, ld=ld, **kw)
