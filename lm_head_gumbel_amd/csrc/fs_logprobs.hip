@@ -80,7 +80,8 @@ struct Chunk {
     }
     __device__ __forceinline__ int id(int e) const { return first + lane0 + e * step; }
 };
-// Its elements (-inf past the end; STREAM: read past the caches), and bit e of `bits`: element e is allowed.
+// Its elements (-inf past the end; STREAM: read past the caches), and bit e of
+// `bits`: element e is allowed.
 template <int DT, bool MASKED, bool STREAM>
 __device__ __forceinline__ void load_chunk(const Chunk<DT>& c,
                                            const typename Elem<DT>::type* row,
@@ -254,18 +255,25 @@ struct TopShared {
     int owner[kHeld];
     float tmax[kLpThreads];
     int first[kLpThreads];
-    uint32_t offer[kLpWaves];
+    uint32_t offer[kLpWaves], alone[kLpWaves];
     int threads, count, tied, id_limit;
     uint32_t bound;
 };
 
-// This wave's offer, before the barrier that ends the maxima.
+// This wave's offer, before the barrier that ends the maxima.  Where the row
+// ends inside the slice (ragged: the same for all threads), waves without
+// elements make the lowest offer worthless; the n-th largest of one wave's
+// maxima is such a value too.
 template <int E>
-__device__ __forceinline__ void offer_bound(TopShared<E>& s, float tmax, int n) {
+__device__ __forceinline__ void offer_bound(TopShared<E>& s, float tmax, int n, bool ragged) {
     const uint32_t k[1] = {float_to_ordered(tmax + 0.f)};
     int reach;
     const uint32_t b = nth_largest(k, (n + kLpWaves - 1) / kLpWaves, reach);
-    if ((threadIdx.x & 63) == 0) s.offer[threadIdx.x >> 6] = b;
+    const uint32_t alone = ragged ? nth_largest(k, n, reach) : 0;
+    if ((threadIdx.x & 63) == 0) {
+        s.offer[threadIdx.x >> 6] = b;
+        s.alone[threadIdx.x >> 6] = alone;
+    }
     if (threadIdx.x == 0) s.threads = s.count = 0;
 }
 
@@ -290,6 +298,8 @@ __device__ __forceinline__ uint32_t hold_offers(TopShared<E>& s, const float (&x
     uint32_t bound = s.offer[0];
 #pragma unroll
     for (int w = 1; w < kLpWaves; ++w) bound = min(bound, s.offer[w]);
+#pragma unroll
+    for (int w = 0; w < kLpWaves; ++w) bound = max(bound, s.alone[w]);
     bound = max(bound, float_to_ordered(-INFINITY) + 1);   // unmasked values only
     hold(s, x, float_to_ordered(tmax + 0.f) >= bound);
     return bound;
@@ -435,7 +445,7 @@ __global__ __launch_bounds__(kLpThreads, 7) void logprobs_kernel(LogprobsArgs a,
         tmax = fminf(tmax, kMaxFloat);
         const float wmax = wave_max(tmax);
         if (lane == 0) smax[wave] = wmax;
-        if constexpr (TOP) offer_bound<E>(top, tmax, a.n_top);
+        if constexpr (TOP) offer_bound<E>(top, tmax, a.n_top, base + kLpThreads * E > n);
         __syncthreads();
         const float m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
         uint32_t bound = 0;
@@ -766,8 +776,10 @@ bool past_caches(int B, int V, int dtype) {
 }
 
 int slice_elems(int B, int V, int cus) {
-    // one slice where a workgroup holds the whole row (no second kernel);
-    // long slices once they fill the chip
+    // one slice where a workgroup holds the whole row (no second kernel); long
+    // slices once they fill the chip, twice over: fewer candidates to join
+    // (V = 151936 FP32, long against short: 32 rows 10.5 and 10.1 us, with 5
+    // alternatives 15.4 and 19.6 us; 8 rows 8.8 and 7.3 us, 13.3 and 14.2 us)
     const int64_t one = (int64_t)kLpThreads * kLpLong;
     if (V <= kLpThreads * kLpShort) return kLpThreads * kLpShort;
     if (V <= one || (int64_t)B * ((V + one - 1) / one) >= 2 * cus) return (int)one;
