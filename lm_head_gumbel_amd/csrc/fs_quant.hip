@@ -539,11 +539,17 @@ QuantPlan quant_plan(const QuantArgs& a, int cus) {
         return p.h_bytes + p.s_bytes;
     };
     p.C = p.nb == 1 ? a.B : 16 * p.nb;
-    // waves along k: as many as have kQDepth blocks each.  Rows lie d / 2
-    // bytes apart, so the waves that share them read longer runs of fewer
-    // rows
+    // waves along k (kQDepth blocks each at least).  With several row blocks a
+    // wave as many as can be: rows lie d / 2 bytes apart, so the waves that
+    // share them read longer runs of fewer rows (B=1, d=4096, V=151936: 72 us,
+    // unsplit 82 us).  With fewer, as many as give each wave one row block: a
+    // pass over W then ends in one step (V=32000: unsplit 18, split by 8 23 us;
+    // V=4000: 14 and 7 us)
+    const int waves = cus * kQWaves;
     p.ksplit = 1;
-    while (p.ksplit < kQWaves && 2 * p.ksplit * kQDepth <= nkb) p.ksplit *= 2;
+    while (p.ksplit < kQWaves && 2 * p.ksplit * kQDepth <= nkb &&
+           (nmb > 2 * waves || 2 * p.ksplit * nmb <= waves))
+        p.ksplit *= 2;
     p.nkb = round_up(nkb, kQDepth * p.ksplit);
     auto rest = [&](int mr) {   // scales, totals
         return (size_t)kQWaves * mr * (pair_slots(p.nb, ns) * ns * 16 * 8) +
