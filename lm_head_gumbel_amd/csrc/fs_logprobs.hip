@@ -10,6 +10,9 @@
 // into registers (E elements a thread, all loads issued before the first
 // use), so the slice's maximum is known before the first exponential and no
 // running sum is ever rescaled; a second kernel joins the slices of a row.
+// MI355X: 2048 x 128256 bf16 in 142 us, 3.7 TB/s, where the exponential of
+// every element (a quarter-rate instruction) bounds it; 4096 x 32000 FP32 in 89
+// us, 5.9 TB/s; 1 x 151936 FP32 with 20 alternatives in 14 us, all latency.
 #include <algorithm>
 #include <type_traits>
 
@@ -655,7 +658,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LogprobsArgs 
 
 // Gradient: dl_i = 1/T [ p_i (c - g_H (ln p_i + H)) + [i = token] g_lp +
 // sum_j [i = top_j] g_top_j ],  c = g_lse - g_lp - sum_j g_top_j, ln p_i = x_i
-// - lse.  Bound by one read and one write of [B, V].
+// - lse.  Bound by one read and one write of [B, V]: 2048 x 151936 bf16 in 243
+// us, 5.1 TB/s.
 constexpr int kGradElems = 16;   // per thread
 constexpr int kSpecials = kMaxAlternatives + 1;
 

@@ -15,6 +15,12 @@
 // in FP32: no weight is rounded), and one multiply-add with s adds the group
 // to the row's total.  H lies in LDS in operand order, its k permuted as the
 // words unpack.
+//
+// MI355X: B=1, d=4096, V=151936, group 128 in 65 us, 5.0 TB/s, what a large
+// copy reaches.  B=64, d=5120, V=152057, group 64 in 221 to 243 us, 410 to 450
+// TFLOP/s: bound by the vector and LDS instructions beside the matrix ones
+// (unpacking, a start and a multiply-add per group and tile) with two waves a
+// SIMD.
 #include "fs_vocab.h"
 
 #include "fs_internal.h"
@@ -41,7 +47,9 @@ struct QuantPlan {
     int nkb;       // k blocks of 128, padded to a multiple of kQDepth ksplit
     int KC;        // k blocks per LDS chunk
     int nchunks;
-    int mr;        // 16-row blocks per wave and pass
+    int mr;        // 16-row blocks per wave and pass: 2 where H passes through LDS
+                   // in chunks, which both use; else 1 (two measured the same or
+                   // up to 12% slower, with half the waves a SIMD can hold)
     int ksplit;    // waves that share a row block (resident only)
     bool chunked;  // H passes through LDS in chunks (else it stays there whole)
     int G;         // workgroups along V
@@ -528,6 +536,8 @@ constexpr size_t kQLds = 160 * 1024;
 
 QuantPlan quant_plan(const QuantArgs& a, int cus) {
     QuantPlan p{};
+    // four column blocks from 33 columns on (two would read W twice: B=64,
+    // d=5120, V=152057 300 against 240 us)
     p.nb = a.B <= 16 ? 1 : a.B <= 32 ? 2 : 4;
     const int nkb = (a.d + kQBlock - 1) / kQBlock;
     const int ns = a.group >= 128 ? 1 : 128 / a.group;
@@ -555,18 +565,16 @@ QuantPlan quant_plan(const QuantArgs& a, int cus) {
         return (size_t)kQWaves * mr * (pair_slots(p.nb, ns) * ns * 16 * 8) +
                (p.ksplit > 1 ? (size_t)2 * kQWaves * mr * p.nb * 64 * 16 : 0);
     };
-    p.mr = 2;
-    while (p.mr > 1 && (nmb + p.mr - 1) / p.mr < cus * (kQWaves / p.ksplit)) p.mr /= 2;
-    while (p.mr > 1 && bytes(p.nkb) + rest(p.mr) > kQLds) p.mr /= 2;
-    p.chunked = p.nb == 4 || bytes(p.nkb) + rest(p.mr) > kQLds;
+    p.mr = 1;
+    p.chunked = p.nb == 4 || bytes(p.nkb) + rest(1) > kQLds;
     if (!p.chunked) {
         p.KC = p.nkb;
         p.nchunks = 1;
-        p.pair_off = bytes(p.KC) + rest(p.mr) - (size_t)kQWaves * p.mr * (pair_slots(p.nb, ns) * ns * 16 * 8);
-        p.lds = bytes(p.KC) + rest(p.mr);
+        p.lds = bytes(p.KC) + rest(1);
+        p.pair_off = p.lds - (size_t)kQWaves * (pair_slots(p.nb, ns) * ns * 16 * 8);
         int occ = (int)(kQLds / p.lds);
         if (occ > 2) occ = 2;
-        p.per_pass = (kQWaves / p.ksplit) * p.mr;
+        p.per_pass = kQWaves / p.ksplit;
         const int ntile = (nmb + p.per_pass - 1) / p.per_pass;
         p.G = ntile < cus * occ ? ntile : cus * occ;
     } else {
@@ -653,13 +661,10 @@ hipError_t launch_quant(const QuantArgs& a, int cus, hipStream_t stream) {
         return hipGetLastError();
     }
     const QuantPlan p = quant_plan(a, cus);
-    if (p.nb == 1)
-        return p.mr == 2 ? launch_nb<1, 2, false>(a, p, stream)
-                         : launch_nb<1, 1, false>(a, p, stream);
-    if (p.chunked)
-        return p.nb == 2 ? launch_nb<2, 2, true>(a, p, stream)
-                         : launch_nb<4, 2, true>(a, p, stream);
-    return p.mr == 2 ? launch_nb<2, 2, false>(a, p, stream) : launch_nb<2, 1, false>(a, p, stream);
+    if (!p.chunked)
+        return p.nb == 1 ? launch_nb<1, 1, false>(a, p, stream)
+                         : launch_nb<2, 1, false>(a, p, stream);
+    return p.nb == 2 ? launch_nb<2, 2, true>(a, p, stream) : launch_nb<4, 2, true>(a, p, stream);
 }
 
 }  // namespace fs
